@@ -22,6 +22,16 @@ is no CPU fallback: if the library is not built, loading raises.
     gq_moe_scatter(Yb, pos, w, k, out)                 -> out[t] += sum_j w Yb[pos[t k + j]]
     gq_matmul_experts_dev(fmt, W, n_expert, rows, cols, X, counts, Y=None)
                                                        -> gq_matmul_experts, counts on the device
+    gq_rope_freqs(rot, base, ...)                      -> (inverse frequencies, mscale), on the host
+    gq_qk_rope(x, pos, rope, norm=None, ...)           -> heads normed and rotated
+    gq_kv4_page_bytes(page_tokens, n_kv, head_dim)     -> bytes of a page of the 4-bit cache
+    gq_kv4_append(cache, k, v, lens, q_start, ...)     -> keys rotated and stored, values stored
+    gq_kv4_read(cache, lens, n_tok, q_start)           -> (K, V) fp32, the values held
+    gq_kv4_attn_ws_bytes(cache, n_head, max_q, max_len) -> workspace of gq_kv4_attn
+    gq_kv4_attn(cache, q, lens, q_start, ...)          -> attention over the cache
+
+KV4Cache is the paged 4-bit key/value cache (pages and page table), Rope a
+rotation; both are plain handles on the caller's tensors.
 
 W is a uint8 CUDA tensor holding rows * gq_row_bytes(fmt, cols) bytes of
 GGUF blocks; fmt is FMT_Q8_0 (8), FMT_Q4_K (12), FMT_Q5_0 (6), FMT_Q5_K (13)
@@ -57,9 +67,29 @@ EXPORTS = ("gq_row_bytes", "gq_status_str", "gq_dequant", "gq_matvec", "gq_matve
            "gq_matvec_swiglu", "gq_matvec_experts", "gq_matvec_batch", "gq_q8_0_split_repack",
            "gq_matmul", "gq_matmul_experts", "gq_quantize_q8_1", "gq_matvec_q8_1",
            "gq_matmul_acc", "gq_matmul_swiglu", "gq_moe_bucket", "gq_moe_gather", "gq_moe_scatter",
-           "gq_matmul_experts_dev")
+           "gq_matmul_experts_dev", "gq_rope_freqs", "gq_qk_rope", "gq_kv4_page_bytes", "gq_kv4_append",
+           "gq_kv4_read", "gq_kv4_attn_ws_bytes", "gq_kv4_attn")
+
+# gq_rope_freqs' scalings
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_BANDS = 2
+ROPE_YARN = 3
 
 _lib = None
+
+
+class _RopeStruct(ctypes.Structure):
+    """gq_rope of gq.h."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot", ctypes.c_int64), ("interleaved", ctypes.c_int32),
+                ("mscale", ctypes.c_float)]
+
+
+class _KV4Struct(ctypes.Structure):
+    """gq_kv4 of gq.h."""
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_tokens", ctypes.c_int64),
+                ("n_kv", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("n_seq", ctypes.c_int64)]
 
 
 class GQError(RuntimeError):
@@ -108,6 +138,21 @@ def load_library():
     lib.gq_moe_scatter.restype = i32
     lib.gq_matmul_experts_dev.argtypes = [i32, vp, i64, i64, i64, vp, vp, i64, vp, vp]
     lib.gq_matmul_experts_dev.restype = i32
+    f32, f64 = ctypes.c_float, ctypes.c_double
+    lib.gq_rope_freqs.argtypes = [i64, f64, i32, f64, f64, f64, f64, vp, vp]
+    lib.gq_rope_freqs.restype = i32
+    lib.gq_qk_rope.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, f32, vp, i64, vp]
+    lib.gq_qk_rope.restype = i32
+    lib.gq_kv4_page_bytes.argtypes = [i64, i64, i64]
+    lib.gq_kv4_page_bytes.restype = i64
+    lib.gq_kv4_append.argtypes = [vp, vp, i64, vp, i64, i64, vp, vp, vp, vp, vp, i64, i64, vp, vp, i64, f32, vp]
+    lib.gq_kv4_append.restype = i32
+    lib.gq_kv4_read.argtypes = [vp, i64, vp, vp, vp, vp, vp]
+    lib.gq_kv4_read.restype = i32
+    lib.gq_kv4_attn_ws_bytes.argtypes = [vp, i64, i64, i64]
+    lib.gq_kv4_attn_ws_bytes.restype = i64
+    lib.gq_kv4_attn.argtypes = [vp, vp, i64, i64, i64, vp, vp, i64, i64, f32, i32, i64, vp, i64, vp, i64, vp]
+    lib.gq_kv4_attn.restype = i32
     _lib = lib
     return lib
 
@@ -454,3 +499,248 @@ def gq_matmul_experts_dev(fmt: int, W, n_expert: int, rows: int, cols: int, X, c
     if st != GQ_OK:
         raise GQError(st, "gq_matmul_experts_dev")
     return Y
+
+
+# ------------------------------------------- rotary positions, 4-bit cache
+def gq_rope_freqs(rot: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+                  orig_ctx: float = 0.0, lo: float = 1.0, hi: float = 4.0):
+    """(fp32 CPU tensor of rot / 2 inverse frequencies, mscale); scaling is
+    ROPE_PLAIN, ROPE_LINEAR, ROPE_BANDS or ROPE_YARN. Computed on the host."""
+    torch = _torch()
+    freqs = torch.empty(max(0, int(rot)) // 2, dtype=torch.float32)
+    mscale = ctypes.c_float(1.0)
+    st = load_library().gq_rope_freqs(int(rot), float(base), int(scaling), float(factor), float(orig_ctx),
+                                      float(lo), float(hi), _ptr(freqs) or None, ctypes.addressof(mscale))
+    if st != GQ_OK:
+        raise GQError(st, "gq_rope_freqs")
+    return freqs, float(mscale.value)
+
+
+class Rope:
+    """A rotation: freqs (fp32 GPU tensor of rot / 2 inverse frequencies, see
+    gq_rope_freqs), the pairing (interleaved: channels 2p, 2p + 1; else p, p +
+    rot / 2) and the scale of the rotated channels. A handle on freqs, which
+    is read when a kernel runs."""
+
+    def __init__(self, freqs, interleaved: bool = False, mscale: float = 1.0):
+        _check_dev(freqs, "freqs", _torch().float32)
+        self.freqs, self.rot = freqs, 2 * freqs.numel()
+        self.interleaved, self.mscale = bool(interleaved), float(mscale)
+        self._struct = _RopeStruct(_ptr(freqs), self.rot, int(self.interleaved), self.mscale)
+        self._ref = ctypes.addressof(self._struct)
+
+
+class KV4Cache:
+    """A paged key/value cache in 4-bit blocks: pages (uint8 GPU tensor of
+    n_pages * gq_kv4_page_bytes(page_tokens, n_kv, head_dim) bytes) and the
+    page table (int32 GPU tensor [n_seq, pages per sequence]). A handle on
+    both tensors, whose contents are read and written when a kernel runs."""
+
+    def __init__(self, pages, table, page_tokens: int, n_kv: int, head_dim: int):
+        torch = _torch()
+        _check_dev(pages, "pages", torch.uint8)
+        _check_dev(table, "table", torch.int32)
+        if table.dim() != 2:
+            raise ValueError("table must be [n_seq, pages per sequence]")
+        self.page_bytes = gq_kv4_page_bytes(page_tokens, n_kv, head_dim)
+        if self.page_bytes < 0:
+            raise GQError(GQ_ERR_SHAPE, "KV4Cache")
+        if pages.numel() % self.page_bytes:
+            raise ValueError(f"pages must hold whole pages of {self.page_bytes} bytes")
+        self.pages, self.table = pages, table
+        self.n_pages = pages.numel() // self.page_bytes
+        self.page_tokens, self.n_kv, self.head_dim = int(page_tokens), int(n_kv), int(head_dim)
+        self.n_seq, self.capacity = table.shape[0], table.shape[1] * self.page_tokens
+        self._struct = _KV4Struct(_ptr(pages), self.n_pages, self.page_tokens, self.n_kv, self.head_dim,
+                                  _ptr(table), table.shape[1], self.n_seq)
+        self._ref = ctypes.addressof(self._struct)
+
+
+def gq_kv4_page_bytes(page_tokens: int, n_kv: int, head_dim: int) -> int:
+    return int(load_library().gq_kv4_page_bytes(int(page_tokens), int(n_kv), int(head_dim)))
+
+
+def _heads(t, name, dev):
+    """The token stride of a [tokens, heads, head_dim] fp32 tensor whose
+    heads lie one after another."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device, cuda:{dev}")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return st if n > 1 else h * d
+
+
+def _flat(t, name, dtype, n, dev):
+    """The address of a contiguous GPU tensor of at least n values (None: 0)."""
+    if t is None:
+        return None
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device, cuda:{dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < n:
+        raise ValueError(f"{name} is too small")
+    return t.data_ptr()
+
+
+def _rope_ref(rope, dev):
+    if rope is None:
+        return None
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    if rope.freqs.get_device() != dev:
+        raise ValueError(f"rope must be on the current device, cuda:{dev}")
+    return rope._ref
+
+
+def _batch(cache, lens, q_start, n_tok, dev):
+    """Addresses of q_start and lens for n_tok rows over the cache."""
+    torch = _torch()
+    if not isinstance(cache, KV4Cache):
+        raise TypeError("cache must be a KV4Cache")
+    if cache.pages.get_device() != dev:
+        raise ValueError(f"cache must be on the current device, cuda:{dev}")
+    if q_start is None and n_tok != cache.n_seq:
+        raise ValueError("without q_start there is one row per sequence")
+    return (_flat(q_start, "q_start", torch.int32, cache.n_seq + 1, dev),
+            _flat(lens, "lens", torch.int32, cache.n_seq, dev))
+
+
+def gq_qk_rope(x, pos, rope=None, norm=None, eps: float = 1e-6, out=None, stream=None):
+    """x [tokens, heads, head_dim] normed per head (norm: head_dim weights)
+    and rotated to the positions pos (int32 [tokens]); out may be x.
+    Asynchronous."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    xs = _heads(x, "x", dev)
+    n, h, d = x.shape
+    if out is None:
+        out = torch.empty((n, h, d), dtype=torch.float32, device=x.device)
+    os_ = _heads(out, "out", dev)
+    if out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    st = load_library().gq_qk_rope(x.data_ptr(), xs, n, h, d, _flat(pos, "pos", torch.int32, n, dev),
+                                   _rope_ref(rope, dev), _flat(norm, "norm", torch.float32, d, dev),
+                                   eps, out.data_ptr(), os_, _stream_handle(stream))
+    if st != GQ_OK:
+        raise GQError(st, "gq_qk_rope")
+    return out
+
+
+def gq_kv4_append(cache, k, v, lens, q_start=None, rope=None, k_norm=None, q=None, q_norm=None, q_out=None,
+                  eps: float = 1e-6, stream=None):
+    """Stores keys (normed with k_norm, rotated) and values of k, v [tokens,
+    n_kv, head_dim] at their positions; with q [tokens, heads, head_dim] the
+    same launch norms and rotates the queries into q_out (new if None; may be
+    q), which is returned (else None). Asynchronous."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    ks, vs = _heads(k, "k", dev), _heads(v, "v", dev)
+    n = k.shape[0]
+    starts, lengths = _batch(cache, lens, q_start, n, dev)
+    d = cache.head_dim
+    if k.shape != (n, cache.n_kv, d) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [tokens, {cache.n_kv}, {d}]")
+    qp = qop = None
+    qs = qos = heads = 0
+    if q is not None:
+        qs = _heads(q, "q", dev)
+        heads = q.shape[1]
+        if q.shape[0] != n or q.shape[2] != d:
+            raise ValueError(f"q must be [{n}, heads, {d}]")
+        if q_out is None:
+            q_out = torch.empty((n, heads, d), dtype=torch.float32, device=q.device)
+        qos = _heads(q_out, "q_out", dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    st = load_library().gq_kv4_append(cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, n, starts, lengths,
+                                      _rope_ref(rope, dev),
+                                      _flat(k_norm, "k_norm", torch.float32, d, dev), qp, qs, heads,
+                                      _flat(q_norm, "q_norm", torch.float32, d, dev), qop, qos, eps,
+                                      _stream_handle(stream))
+    if st != GQ_OK:
+        raise GQError(st, "gq_kv4_append")
+    return q_out
+
+
+def gq_kv4_read(cache, lens, n_tok: int, q_start=None, K=None, V=None, stream=None):
+    """(K, V) fp32 [n_tok, n_kv, head_dim]: the values held for the batch's
+    rows. Asynchronous."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    starts, lengths = _batch(cache, lens, q_start, n_tok, dev)
+    shape = (n_tok, cache.n_kv, cache.head_dim)
+    if K is None:
+        K = torch.empty(shape, dtype=torch.float32, device=cache.pages.device)
+    if V is None:
+        V = torch.empty(shape, dtype=torch.float32, device=cache.pages.device)
+    n = n_tok * cache.n_kv * cache.head_dim
+    st = load_library().gq_kv4_read(cache._ref, n_tok, starts, lengths, _flat(K, "K", torch.float32, n, dev),
+                                    _flat(V, "V", torch.float32, n, dev), _stream_handle(stream))
+    if st != GQ_OK:
+        raise GQError(st, "gq_kv4_read")
+    return K, V
+
+
+def gq_kv4_attn_ws_bytes(cache, n_head: int, max_q: int, max_len: int) -> int:
+    """Bytes of workspace that gq_kv4_attn takes for these sizes."""
+    need = int(load_library().gq_kv4_attn_ws_bytes(cache._ref, n_head, max_q, max_len))
+    if need < 0:
+        raise GQError(GQ_ERR_SHAPE, "gq_kv4_attn_ws_bytes")
+    return need
+
+
+def gq_kv4_attn(cache, q, lens, q_start=None, max_q: int = 1, max_len=None, scale=None, causal: bool = True,
+                window: int = 0, out=None, workspace=None, stream=None):
+    """Attention of q [tokens, heads, head_dim] over the cache (head_dim ** -0.5
+    is the default scale, the table's capacity the default max_len). max_q is
+    at least every sequence's rows. workspace: a uint8 GPU tensor of
+    gq_kv4_attn_ws_bytes that no other call in flight uses; None takes one
+    from torch's allocator for this call on its stream. Asynchronous."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    qs = _heads(q, "q", dev)
+    n, heads, d = q.shape
+    starts, lengths = _batch(cache, lens, q_start, n, dev)
+    if d != cache.head_dim:
+        raise ValueError(f"q must be [tokens, heads, {cache.head_dim}]")
+    if out is None:
+        out = torch.empty((n, heads, d), dtype=torch.float32, device=q.device)
+    os_ = _heads(out, "out", dev)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if max_len is None:
+        max_len = cache.capacity
+    lib = load_library()
+    need = lib.gq_kv4_attn_ws_bytes(cache._ref, heads, max_q, max_len)
+    if need < 0:
+        raise GQError(GQ_ERR_SHAPE, "gq_kv4_attn")
+    if workspace is None and need > 0:
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            with torch.cuda.stream(stream):  # freed into the stream that the kernels run on
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = lib.gq_kv4_attn(cache._ref, q.data_ptr(), qs, heads, n, starts, lengths, max_q, max_len,
+                         d ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(), os_,
+                         _flat(workspace, "workspace", torch.uint8, need, dev),
+                         0 if workspace is None else workspace.numel(), _stream_handle(stream))
+    if st != GQ_OK:
+        raise GQError(st, "gq_kv4_attn")
+    return out

@@ -1,0 +1,140 @@
+// kv4.h -- the paged 4-bit key/value cache as the kernels see it: page
+// layout, the block's arithmetic, and the ragged batch that the append, read
+// and attention kernels share. The layout is stated in gq.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gq {
+
+struct Kv4Args {
+  uint8_t* pages;
+  const int32_t* table;
+  const int32_t* q_start;  // null: one row per sequence
+  const int32_t* lens;
+  int64_t page_bytes;
+  int n_pages;
+  int page_log2;
+  int n_kv;
+  int hd;
+  int table_stride;
+  int n_seq;
+  int n_tok;
+};
+
+struct RopeArgs {
+  const float* freqs;
+  int half;  // pairs that rotate (rot / 2)
+  int interleaved;
+  float mscale;
+};
+
+// Heads that are normed and rotated into fp32 (queries), or appended.
+struct HeadArgs {
+  const float* x;
+  const float* w;  // norm weights, or null
+  float* out;
+  int64_t x_stride;
+  int64_t out_stride;
+  int n_head;
+};
+
+struct AttnArgs {
+  Kv4Args c;
+  const float* q;
+  float* out;
+  int64_t q_stride;
+  int64_t out_stride;
+  int n_head;
+  int group;    // query heads per kv head
+  int max_q;
+  int max_len;
+  float scale;  // softmax scale times log2(e): weights are powers of two
+  int causal;
+  int window;   // 0: none
+  int splits;   // parts that a sequence's keys are cut into
+  float* part;  // splits > 1: the parts' sums, and after them their (maximum, total)
+};
+
+hipError_t launch_qk_rope(const HeadArgs& h, int n_tok, int hd, const int32_t* pos, const RopeArgs& r, float eps,
+                          hipStream_t s);
+hipError_t launch_kv4_append(const Kv4Args& c, const HeadArgs& q, const HeadArgs& k, const HeadArgs& v,
+                             const RopeArgs& r, float eps, hipStream_t s);
+hipError_t launch_kv4_read(const Kv4Args& c, float* K, float* V, hipStream_t s);
+// Into how many parts the attention cuts each sequence (1: none, no
+// workspace), and its workspace: the parts' sums and their (maximum, total).
+int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len);
+hipError_t launch_kv4_attn(const AttnArgs& a, hipStream_t s);
+
+// Where the codes and scales of one kv head's keys (kv = 0) or values (kv =
+// 1) start inside a page; code rows are hd / 2 bytes, scale rows (one per
+// block of 32 channels) a page's tokens of fp16.
+__host__ __device__ inline int kv4_code_bytes(int hd, int page_log2) { return (hd / 2) << page_log2; }
+__host__ __device__ inline int kv4_part_bytes(int hd, int page_log2) {
+  return (hd / 2 + hd / 16) << page_log2;
+}
+__host__ __device__ inline int64_t kv4_part(const Kv4Args& c, int head, int kv) {
+  return (int64_t)(2 * head + kv) * kv4_part_bytes(c.hd, c.page_log2);
+}
+
+// The rows and the length of one sequence, as the device arrays give them.
+struct SeqRows {
+  int first;  // its first row
+  int n;      // its rows (negative offsets or descending ones: none)
+  int len;    // tokens in the cache
+};
+
+__device__ __forceinline__ SeqRows seq_rows(const Kv4Args& c, int b) {
+  SeqRows s;
+  if (c.q_start) {
+    const int64_t lo = c.q_start[b], hi = c.q_start[b + 1];
+    const bool ok = lo >= 0 && hi >= lo && hi <= c.n_tok;
+    s.first = ok ? (int)lo : 0;
+    s.n = ok ? (int)(hi - lo) : 0;
+  } else {
+    s.first = b;
+    s.n = 1;
+  }
+  s.len = c.lens[b];
+  return s;
+}
+
+// The position of token row t, and its sequence; -1 where the row belongs to
+// none. The offsets are searched 64 at a time (one load per lane and a
+// ballot), so a batch of up to 64 sequences costs one round trip.
+__device__ __forceinline__ int row_position(const Kv4Args& c, int t, int* seq) {
+  int b = t;
+  if (c.q_start) {
+    // the last b with q_start[b] <= t
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = c.n_seq + 1;
+    while (n > 1) {
+      const int step = (n + 63) / 64;
+      const int i = lo + lane * step;
+      const uint64_t m = __ballot(lane * step < n && c.q_start[i < c.n_seq ? i : c.n_seq] <= t);
+      if (m == 0) return -1;
+      const int at = 63 - __clzll((unsigned long long)m);
+      const int end = lo + n;
+      lo += at * step;
+      n = step < end - lo ? step : end - lo;
+    }
+    b = lo;
+  }
+  if (b >= c.n_seq) return -1;
+  const SeqRows s = seq_rows(c, b);
+  const int64_t i = (int64_t)t - s.first;
+  if (i < 0 || i >= s.n) return -1;
+  const int64_t p = (int64_t)s.len - s.n + i;
+  if (p < 0 || p >= ((int64_t)c.table_stride << c.page_log2)) return -1;
+  *seq = b;
+  return (int)p;
+}
+
+// The page of position p of sequence b, or null where its number is not one.
+__device__ __forceinline__ uint8_t* page_of(const Kv4Args& c, int b, int p) {
+  const int id = c.table[(int64_t)b * c.table_stride + (p >> c.page_log2)];
+  return id >= 0 && id < c.n_pages ? c.pages + id * c.page_bytes : nullptr;
+}
+
+}  // namespace gq

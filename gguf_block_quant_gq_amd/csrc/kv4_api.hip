@@ -1,0 +1,305 @@
+// kv4_api.hip -- the extern "C" entry points of the rotary positions and the
+// paged 4-bit key/value cache (declared in gq.h): argument checks on the
+// host, launch. Every check runs before the first HIP call.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/gq.h"
+#include "kv4.h"
+
+namespace {
+
+constexpr int64_t kMaxDim = int64_t(1) << 30;  // as for the products: 32-bit indices stay in range
+
+int finish(hipError_t e) { return e == hipSuccess ? GQ_OK : GQ_ERR_DEVICE; }
+
+// A strided matrix in memory: n rows of `width` bytes every `stride` bytes.
+struct Span {
+  const void* p;
+  int64_t n;
+  int64_t width;
+  int64_t stride;
+};
+
+Span flat(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+
+// Whether two strided matrices share a byte. Rows of one buffer interleaved
+// at one stride (the parts of a fused projection) are told apart exactly;
+// matrices of different strides by their ends alone.
+bool touch(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.n <= 0 || b.n <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+  const uintptr_t ea = pa + (uintptr_t)((a.n - 1) * a.stride + a.width);
+  const uintptr_t eb = pb + (uintptr_t)((b.n - 1) * b.stride + b.width);
+  if (pa >= eb || pb >= ea) return false;
+  if (a.n == 1 && b.n == 1) return true;
+  const int64_t s = a.n > 1 ? a.stride : b.stride;
+  if ((a.n > 1 && a.stride != s) || (b.n > 1 && b.stride != s)) return true;
+  // where b's rows begin inside a's, modulo the stride
+  const uintptr_t m = (uintptr_t)s;
+  const int64_t off = (int64_t)(pb >= pa ? (pb - pa) % m : (m - (pa - pb) % m) % m);
+  return off < a.width || off + b.width > s;
+}
+
+// n rows of `width` floats every `stride` floats: a stride that holds a row
+// (any, for a single row), sizes that 64 bits hold.
+bool rows_ok(int64_t n, int64_t width, int64_t stride) {
+  if (n <= 1) return stride >= 0 && stride <= (int64_t(1) << 40);
+  return stride >= width && stride <= (int64_t(1) << 40) && n <= INT64_MAX / 8 / stride;
+}
+
+Span rows_of(const float* p, int64_t n, int64_t width, int64_t stride) {
+  return {p, n, width * 4, n > 1 ? stride * 4 : width * 4};
+}
+
+// A rotation for heads of head_dim channels; on success *r is what the
+// kernels take. No rotation: half = 0.
+int check_rope(const gq_rope* rope, int64_t head_dim, gq::RopeArgs* r) {
+  *r = gq::RopeArgs{nullptr, 0, 0, 1.f};
+  if (!rope) return GQ_OK;
+  if (rope->rot < 0 || rope->rot > head_dim || rope->rot % 2) return GQ_ERR_SHAPE;
+  if (rope->interleaved != 0 && rope->interleaved != 1) return GQ_ERR_SHAPE;
+  if (rope->rot == 0) return GQ_OK;
+  if (!rope->freqs) return GQ_ERR_NULL;
+  if ((uintptr_t)rope->freqs % 4) return GQ_ERR_ALIGN;
+  *r = gq::RopeArgs{rope->freqs, (int)(rope->rot / 2), rope->interleaved, rope->mscale};
+  return GQ_OK;
+}
+
+// The cache and the ragged batch of n_tok rows; on success *c is what the
+// kernels take (pointers still to be checked with check_cache_ptrs).
+int check_cache(const gq_kv4* cache, int64_t n_tok, const int32_t* q_start, const int32_t* lens, gq::Kv4Args* c) {
+  if (!cache) return GQ_ERR_NULL;
+  const int64_t pb = gq_kv4_page_bytes(cache->page_tokens, cache->n_kv, cache->head_dim);
+  if (pb < 0) return GQ_ERR_SHAPE;
+  if (cache->n_pages < 0 || cache->n_pages > kMaxDim || cache->n_pages > INT64_MAX / 2 / pb) return GQ_ERR_SHAPE;
+  if (cache->n_seq < 0 || cache->n_seq > kMaxDim || n_tok < 0 || n_tok > kMaxDim) return GQ_ERR_SHAPE;
+  if (cache->table_stride < 0 || cache->table_stride > kMaxDim / cache->page_tokens) return GQ_ERR_SHAPE;
+  if (!q_start && n_tok != cache->n_seq) return GQ_ERR_SHAPE;
+  int log2 = 0;
+  while ((int64_t(1) << log2) < cache->page_tokens) ++log2;
+  c->pages = (uint8_t*)cache->pages;
+  c->table = cache->table;
+  c->q_start = q_start;
+  c->lens = lens;
+  c->page_bytes = pb;
+  c->n_pages = (int)cache->n_pages;
+  c->page_log2 = log2;
+  c->n_kv = (int)cache->n_kv;
+  c->hd = (int)cache->head_dim;
+  c->table_stride = (int)cache->table_stride;
+  c->n_seq = (int)cache->n_seq;
+  c->n_tok = (int)n_tok;
+  return GQ_OK;
+}
+
+int check_cache_ptrs(const gq::Kv4Args& c) {
+  if ((!c.pages && c.n_pages > 0) || (!c.table && c.n_seq > 0 && c.table_stride > 0) || (!c.lens && c.n_seq > 0))
+    return GQ_ERR_NULL;
+  if ((uintptr_t)c.pages % 16 || (uintptr_t)c.table % 4 || (uintptr_t)c.lens % 4 || (uintptr_t)c.q_start % 4)
+    return GQ_ERR_ALIGN;
+  return GQ_OK;
+}
+
+Span pages_of(const gq::Kv4Args& c) { return flat(c.pages, c.n_pages * c.page_bytes); }
+
+// Whether an output touches the arrays that say where rows and pages are.
+bool touches_index(const Span& o, const gq::Kv4Args& c) {
+  return touch(o, flat(c.table, (int64_t)c.n_seq * c.table_stride * 4)) || touch(o, flat(c.lens, (int64_t)c.n_seq * 4)) ||
+         touch(o, flat(c.q_start, c.q_start ? ((int64_t)c.n_seq + 1) * 4 : 0));
+}
+
+}  // namespace
+
+extern "C" int gq_rope_freqs(int64_t rot, double base, int scaling, double factor, double orig_ctx, double lo,
+                             double hi, float* freqs, float* mscale) {
+  if (rot < 0 || rot % 2 || rot > (int64_t(1) << 20)) return GQ_ERR_SHAPE;
+  if (scaling < GQ_ROPE_PLAIN || scaling > GQ_ROPE_YARN) return GQ_ERR_SHAPE;
+  if (!(base > 1.0) || !std::isfinite(base)) return GQ_ERR_SHAPE;
+  if (scaling != GQ_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return GQ_ERR_SHAPE;
+  if (scaling >= GQ_ROPE_BANDS &&
+      (!(orig_ctx > 0.0) || !std::isfinite(orig_ctx) || !(lo > 0.0) || !(hi > lo) || !std::isfinite(hi)))
+    return GQ_ERR_SHAPE;
+  if (rot > 0 && !freqs) return GQ_ERR_NULL;
+  const double two_pi = 6.283185307179586476925;
+  // YaRN: the pair index at which a pair makes `turns` turns over orig_ctx
+  const auto pair_at = [&](double turns) {
+    return (double)rot * std::log(orig_ctx / (turns * two_pi)) / (2.0 * std::log(base));
+  };
+  double first = 0.0, last = 1.0;
+  if (scaling == GQ_ROPE_YARN) {
+    first = std::fmax(std::floor(pair_at(hi)), 0.0);
+    last = std::fmin(std::ceil(pair_at(lo)), (double)rot - 1.0);
+    if (!(last > first)) last = first + 0.001;  // an empty ramp is a step
+  }
+  for (int64_t p = 0; p < rot / 2; ++p) {
+    const double f = std::pow(base, -2.0 * (double)p / (double)rot);
+    double keep = 1.0;  // the share that is not interpolated
+    if (scaling == GQ_ROPE_LINEAR) keep = 0.0;
+    if (scaling == GQ_ROPE_BANDS) keep = (orig_ctx * f / two_pi - lo) / (hi - lo);
+    if (scaling == GQ_ROPE_YARN) keep = 1.0 - ((double)p - first) / (last - first);
+    keep = std::fmin(1.0, std::fmax(0.0, keep));
+    freqs[p] = (float)(scaling == GQ_ROPE_PLAIN ? f : f / factor * (1.0 - keep) + f * keep);
+  }
+  if (mscale) *mscale = scaling == GQ_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+  return GQ_OK;
+}
+
+extern "C" int gq_qk_rope(const float* x, int64_t x_stride, int64_t n_tok, int64_t n_head, int64_t head_dim,
+                          const int32_t* pos, const gq_rope* rope, const float* w, float eps, float* out,
+                          int64_t out_stride, void* stream) {
+  if (head_dim < 8 || head_dim > 256 || head_dim % 8) return GQ_ERR_SHAPE;
+  if (n_tok < 0 || n_tok > kMaxDim || n_head < 0 || n_head > kMaxDim / head_dim) return GQ_ERR_SHAPE;
+  const int64_t width = n_head * head_dim;
+  if (!rows_ok(n_tok, width, x_stride) || !rows_ok(n_tok, width, out_stride)) return GQ_ERR_SHAPE;
+  if (w && !(eps >= 0.f)) return GQ_ERR_SHAPE;
+  gq::RopeArgs r;
+  int st = check_rope(rope, head_dim, &r);
+  if (st != GQ_OK) return st;
+  if (n_tok == 0 || n_head == 0) return GQ_OK;
+  if (!x || !out || (r.half > 0 && !pos)) return GQ_ERR_NULL;
+  if ((uintptr_t)x % 4 || (uintptr_t)out % 4 || (uintptr_t)w % 4 || (uintptr_t)pos % 4) return GQ_ERR_ALIGN;
+  const Span so = rows_of(out, n_tok, width, out_stride), sx = rows_of(x, n_tok, width, x_stride);
+  const bool in_place = x == out && so.stride == sx.stride;
+  if ((!in_place && touch(so, sx)) || touch(so, flat(w, head_dim * 4)) || touch(so, flat(r.freqs, r.half * 4)) ||
+      (r.half > 0 && touch(so, flat(pos, n_tok * 4))))
+    return GQ_ERR_OVERLAP;
+  (void)hipGetLastError();
+  const gq::HeadArgs h{x, w, out, x_stride, out_stride, (int)n_head};
+  return finish(gq::launch_qk_rope(h, (int)n_tok, (int)head_dim, pos, r, eps, (hipStream_t)stream));
+}
+
+extern "C" int64_t gq_kv4_page_bytes(int64_t page_tokens, int64_t n_kv, int64_t head_dim) {
+  if (page_tokens < 16 || page_tokens > 1024 || (page_tokens & (page_tokens - 1))) return -1;
+  if (head_dim < 32 || head_dim > 256 || head_dim % 32) return -1;
+  if (n_kv < 1 || n_kv > 65535) return -1;
+  return page_tokens * n_kv * (head_dim + head_dim / 8);
+}
+
+extern "C" int gq_kv4_append(const gq_kv4* cache, const float* k, int64_t k_stride, const float* v,
+                             int64_t v_stride, int64_t n_tok, const int32_t* q_start, const int32_t* lens,
+                             const gq_rope* rope, const float* kw, const float* q, int64_t q_stride,
+                             int64_t n_head, const float* qw, float* q_out, int64_t q_out_stride, float eps,
+                             void* stream) {
+  gq::Kv4Args c;
+  int st = check_cache(cache, n_tok, q_start, lens, &c);
+  if (st != GQ_OK) return st;
+  if (!q) n_head = 0;
+  const int64_t kvw = (int64_t)c.n_kv * c.hd;
+  if (n_head < 0 || n_head > kMaxDim / 512) return GQ_ERR_SHAPE;
+  const int64_t qwid = n_head * c.hd;
+  if (!rows_ok(n_tok, kvw, k_stride) || !rows_ok(n_tok, kvw, v_stride)) return GQ_ERR_SHAPE;
+  if (n_head > 0 && (!rows_ok(n_tok, qwid, q_stride) || !rows_ok(n_tok, qwid, q_out_stride))) return GQ_ERR_SHAPE;
+  if ((kw || (qw && n_head > 0)) && !(eps >= 0.f)) return GQ_ERR_SHAPE;
+  gq::RopeArgs r;
+  if ((st = check_rope(rope, c.hd, &r)) != GQ_OK) return st;
+  if (n_tok == 0 || c.n_seq == 0) return GQ_OK;
+  if (!k || !v || (n_head > 0 && !q_out)) return GQ_ERR_NULL;
+  if ((st = check_cache_ptrs(c)) != GQ_OK) return st;
+  if ((uintptr_t)k % 4 || (uintptr_t)v % 4 || (uintptr_t)kw % 4) return GQ_ERR_ALIGN;
+  if (n_head > 0 && ((uintptr_t)q % 4 || (uintptr_t)q_out % 4 || (uintptr_t)qw % 4)) return GQ_ERR_ALIGN;
+  const Span sp = pages_of(c), sk = rows_of(k, n_tok, kvw, k_stride), sv = rows_of(v, n_tok, kvw, v_stride);
+  const Span skw = flat(kw, c.hd * 4), sf = flat(r.freqs, r.half * 4);
+  if (touch(sp, sk) || touch(sp, sv) || touch(sp, skw) || touch(sp, sf) || touches_index(sp, c)) return GQ_ERR_OVERLAP;
+  if (n_head > 0) {
+    const Span sq = rows_of(q, n_tok, qwid, q_stride), so = rows_of(q_out, n_tok, qwid, q_out_stride);
+    const Span sqw = flat(qw, c.hd * 4);
+    const bool in_place = q == q_out && sq.stride == so.stride;
+    if ((!in_place && touch(so, sq)) || touch(so, sk) || touch(so, sv) || touch(so, skw) || touch(so, sqw) ||
+        touch(so, sf) || touch(so, sp) || touches_index(so, c) || touch(sp, sq) || touch(sp, sqw))
+      return GQ_ERR_OVERLAP;
+  }
+  (void)hipGetLastError();
+  const gq::HeadArgs hq{q, qw, q_out, q_stride, q_out_stride, (int)n_head};
+  const gq::HeadArgs hk{k, kw, nullptr, k_stride, 0, c.n_kv};
+  const gq::HeadArgs hv{v, nullptr, nullptr, v_stride, 0, c.n_kv};
+  return finish(gq::launch_kv4_append(c, hq, hk, hv, r, eps, (hipStream_t)stream));
+}
+
+extern "C" int gq_kv4_read(const gq_kv4* cache, int64_t n_tok, const int32_t* q_start, const int32_t* lens,
+                           float* K, float* V, void* stream) {
+  gq::Kv4Args c;
+  int st = check_cache(cache, n_tok, q_start, lens, &c);
+  if (st != GQ_OK) return st;
+  if (n_tok == 0 || c.n_seq == 0 || (!K && !V)) return GQ_OK;
+  if ((st = check_cache_ptrs(c)) != GQ_OK) return st;
+  if ((uintptr_t)K % 4 || (uintptr_t)V % 4) return GQ_ERR_ALIGN;
+  const int64_t bytes = n_tok * c.n_kv * c.hd * 4;  // below 2^30 * 65535 * 2^10
+  const Span sk = flat(K, bytes), sv = flat(V, bytes), sp = pages_of(c);
+  if (touch(sk, sv) || touch(sk, sp) || touch(sv, sp) || touches_index(sk, c) || touches_index(sv, c))
+    return GQ_ERR_OVERLAP;
+  (void)hipGetLastError();
+  return finish(gq::launch_kv4_read(c, K, V, (hipStream_t)stream));
+}
+
+namespace {
+
+// The shape of an attention call: heads, rows per sequence and length bound.
+int check_attn_shape(const gq_kv4* cache, int64_t n_head, int64_t max_q, int64_t max_len) {
+  if (n_head < 1 || n_head > kMaxDim / 512 || n_head % cache->n_kv) return GQ_ERR_SHAPE;
+  if (max_q < 0 || max_q > kMaxDim / n_head) return GQ_ERR_SHAPE;
+  if (max_len < 0 || max_len > cache->table_stride * cache->page_tokens) return GQ_ERR_SHAPE;
+  return GQ_OK;
+}
+
+// Workspace bytes: a sum of head_dim floats, a maximum and a total for every
+// row and part (none when nothing is split); -1 where 64 bits do not hold it.
+int64_t attn_ws(const gq_kv4* cache, int64_t n_head, int64_t max_q, int64_t max_len, int* splits) {
+  const int64_t rows = max_q * (n_head / cache->n_kv);
+  *splits = gq::kv4_attn_splits(cache->n_seq, cache->n_kv, rows, max_len);
+  if (*splits <= 1 || cache->n_seq == 0 || rows == 0) return 0;
+  const int64_t per = (cache->head_dim + 2) * 4 * *splits;
+  if (cache->n_kv * rows > INT64_MAX / per / cache->n_seq) return -1;
+  return cache->n_seq * cache->n_kv * rows * per;
+}
+
+}  // namespace
+
+extern "C" int64_t gq_kv4_attn_ws_bytes(const gq_kv4* cache, int64_t n_head, int64_t max_q, int64_t max_len) {
+  gq::Kv4Args c;
+  int splits = 0;
+  static const int32_t any = 0;  // a ragged batch: its rows do not matter here
+  if (check_cache(cache, 0, &any, nullptr, &c) != GQ_OK) return -1;
+  if (check_attn_shape(cache, n_head, max_q, max_len) != GQ_OK) return -1;
+  return attn_ws(cache, n_head, max_q, max_len, &splits);
+}
+
+extern "C" int gq_kv4_attn(const gq_kv4* cache, const float* q, int64_t q_stride, int64_t n_head, int64_t n_tok,
+                           const int32_t* q_start, const int32_t* lens, int64_t max_q, int64_t max_len, float scale,
+                           int causal, int64_t window, float* out, int64_t out_stride, void* ws, int64_t ws_bytes,
+                           void* stream) {
+  gq::AttnArgs a{};
+  int st = check_cache(cache, n_tok, q_start, lens, &a.c);
+  if (st != GQ_OK) return st;
+  if ((st = check_attn_shape(cache, n_head, max_q, max_len)) != GQ_OK) return st;
+  if (window < 0 || !std::isfinite(scale)) return GQ_ERR_SHAPE;
+  const int64_t width = n_head * a.c.hd;
+  if (!rows_ok(n_tok, width, q_stride) || !rows_ok(n_tok, width, out_stride)) return GQ_ERR_SHAPE;
+  const int64_t need = attn_ws(cache, n_head, max_q, max_len, &a.splits);
+  if (need < 0 || ws_bytes < 0) return GQ_ERR_SHAPE;
+  if (n_tok == 0 || a.c.n_seq == 0 || max_q == 0) return GQ_OK;
+  if (!q || !out || (need > 0 && !ws)) return GQ_ERR_NULL;
+  if (ws_bytes < need) return GQ_ERR_SHAPE;
+  if ((st = check_cache_ptrs(a.c)) != GQ_OK) return st;
+  if ((uintptr_t)q % 4 || (uintptr_t)out % 4 || (need > 0 && (uintptr_t)ws % 16)) return GQ_ERR_ALIGN;
+  const Span so = rows_of(out, n_tok, width, out_stride), sq = rows_of(q, n_tok, width, q_stride);
+  const Span sp = pages_of(a.c), sw = flat(ws, need);
+  if (touch(so, sq) || touch(so, sp) || touches_index(so, a.c) || touch(sw, so) || touch(sw, sq) || touch(sw, sp) ||
+      touches_index(sw, a.c))
+    return GQ_ERR_OVERLAP;
+  (void)hipGetLastError();
+  a.q = q;
+  a.out = out;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.n_head = (int)n_head;
+  a.group = (int)(n_head / a.c.n_kv);
+  a.max_q = (int)max_q;
+  a.max_len = (int)max_len;
+  a.scale = (float)((double)scale * 1.4426950408889634074);  // log2(e)
+  a.causal = causal != 0;
+  a.window = window > kMaxDim ? 0 : (int)window;  // no sequence is longer than 2^30
+  a.part = (float*)ws;
+  return finish(gq::launch_kv4_attn(a, (hipStream_t)stream));
+}

@@ -49,8 +49,9 @@
  * Ownership and threading
  *   All pointers are device pointers owned by the caller; the library never
  *   frees or keeps them. No entry point uses device memory beyond its
- *   arguments: there is no workspace (work split along k stays inside one
- *   workgroup and is added in a fixed order). Global state: a per-device
+ *   arguments: the products have no workspace (work split along k stays
+ *   inside one workgroup and is added in a fixed order), and gq_kv4_attn
+ *   takes its own as an argument. Global state: a per-device
  *   cache of device properties, filled once. Calls on different streams may
  *   run concurrently.
  *
@@ -65,7 +66,8 @@
  *   Q8_0, Q5_0 and Q6_K W: 2-byte aligned (a row range of such a tensor
  *   starts on any block boundary, and their blocks are 34, 22 and 210 bytes).
  *   Q4_K, Q5_K and split Q8_0 W: 4-byte aligned. x, y, X, Y, out: 4-byte
- *   aligned. An output that overlaps an input is rejected (GQ_ERR_OVERLAP).
+ *   aligned. An output that overlaps an input is rejected (GQ_ERR_OVERLAP),
+ *   except where in-place use is stated.
  *
  * Errors
  *   Every entry point returns a gq_status. Arguments are validated on the
@@ -416,6 +418,190 @@ int gq_quantize_q8_1(const float* x, int64_t n, int64_t cols, void* xq, void* st
  */
 int gq_matvec_q8_1(int fmt, const void* W, int64_t rows, int64_t cols, const void* xq, float* y,
                    void* stream);
+
+/*
+ * What stands between the q|k|v projection and the o projection of a
+ * transformer layer: rotary positions with per-head norms, a paged key/value
+ * cache held in 4 bits, and attention over it ("nurllama 0.18.1 API",
+ * kernels.nu section, lists the norms, both rotary layouts and two-pass
+ * attention; the Loom inventory lists QK-norm + RoPE + KV store, split-K
+ * decode attention and a prefill attention). Activations are fp32, as
+ * everywhere in this library; matrices of heads are [tokens, heads, head_dim]
+ * with the heads of a token contiguous and a token stride in floats of the
+ * caller's choice, so that the q, k and v parts of a fused q|k|v projection
+ * are used where they lie.
+ *
+ * gq_rope: the rotation. freqs: rot / 2 inverse frequencies in device memory
+ * (gq_rope_freqs computes them); rot: even, 0 .. head_dim, the leading
+ * channels that rotate (0: none, freqs is not read); interleaved: 0 pairs
+ * channel p with p + rot / 2, 1 pairs 2p with 2p + 1; mscale multiplies the
+ * rotated channels. A token at position pos turns pair p by the angle pos *
+ * freqs[p], (u, v) -> mscale * (u cos - v sin, v cos + u sin). Angle, sine,
+ * cosine, norm and rotation are evaluated in fp64 and rounded once, so far
+ * positions lose nothing.
+ *
+ * Norms: with a weight vector w (head_dim floats) each head first becomes
+ * x_c * w_c / sqrt(mean_c x_c^2 + eps); NULL: no norm.
+ */
+typedef struct gq_rope {
+    const float* freqs;
+    int64_t rot;
+    int32_t interleaved;
+    float mscale;
+} gq_rope;
+
+enum gq_rope_scaling {
+    GQ_ROPE_PLAIN = 0,  /* f_p = base^(-2p / rot) */
+    GQ_ROPE_LINEAR = 1, /* f_p / factor: positions interpolated */
+    GQ_ROPE_BANDS = 2,  /* by wavelength 2 pi / f_p against orig_ctx: below orig_ctx / hi
+                           unchanged, above orig_ctx / lo divided by factor, linear in
+                           orig_ctx / wavelength between */
+    GQ_ROPE_YARN = 3,   /* by turns over orig_ctx (the YaRN paper's "NTK by parts"): pairs
+                           of more than hi turns unchanged, of less than lo divided by
+                           factor, a linear ramp over the pair index between; mscale =
+                           0.1 ln(factor) + 1 */
+};
+
+/*
+ * rot / 2 inverse frequencies into freqs (HOST memory), computed in fp64 and
+ * rounded once, and the mscale that belongs to them (1 except for YARN) into
+ * *mscale (HOST memory, may be NULL). factor >= 1; orig_ctx > 0 and 0 < lo <
+ * hi are read by BANDS and YARN only (customary values: 1 and 4 for BANDS, 1
+ * and 32 for YARN). GQ_ERR_SHAPE for anything outside these ranges, a scaling
+ * that is not listed, an odd or negative rot or one past 2^20, or a base that
+ * is not above 1. Host only.
+ */
+int gq_rope_freqs(int64_t rot, double base, int scaling, double factor, double orig_ctx, double lo, double hi,
+                  float* freqs, float* mscale);
+
+/*
+ * out[t, h] = rotation(norm(x[t, h])) for t < n_tok, h < n_head at position
+ * pos[t] (device, int32, any sign; not read when nothing rotates and then may
+ * be NULL). x_stride, out_stride: floats between tokens, at least n_head *
+ * head_dim. head_dim: 8 .. 256, a multiple of 8. rope NULL: no rotation; w
+ * NULL: no norm (eps is then not read). In place is allowed (out == x with
+ * equal strides); any other overlap of out with an input is GQ_ERR_OVERLAP.
+ * n_tok == 0 or n_head == 0 is a no-op. Each result is within half a step of
+ * fp32 of the formula's value, up to fp64's own rounding. Asynchronous on
+ * `stream`.
+ */
+int gq_qk_rope(const float* x, int64_t x_stride, int64_t n_tok, int64_t n_head, int64_t head_dim,
+               const int32_t* pos, const gq_rope* rope, const float* w, float eps, float* out,
+               int64_t out_stride, void* stream);
+
+/*
+ * gq_kv4: a paged key/value cache in 4-bit blocks. pages: n_pages pages of
+ * gq_kv4_page_bytes bytes (16-byte aligned); page_tokens: tokens a page
+ * holds, a power of two from 16 to 1024; n_kv: key/value heads; head_dim: a
+ * multiple of 32 from 32 to 256. table (device, int32, [n_seq, table_stride]):
+ * entry (b, i) is the page that holds the tokens i * page_tokens .. of
+ * sequence b. table_stride * page_tokens is at most 2^30.
+ *
+ * A block is 32 consecutive channels of one head of one token: a scale d and
+ * 32 codes n in 0..15, value d * (n - 8). With a the block's value of largest
+ * magnitude (the lowest channel among equals), d = -a / 8 rounded to nearest
+ * even to 8 significant bits (never finer than 2^-24), |d| at most 8160, held
+ * as fp16; n - 8 = x / d rounded to nearest even and clamped to -8 .. 7 (0
+ * where d = 0). Eight bits of scale times three of code make every held value
+ * exact in fp16, which is what the attention's matrix products take. Values
+ * past +-65280 saturate; a block with a NaN has a NaN scale. A cache written
+ * elsewhere may hold any fp16 scale: its values are then rounded once to fp16
+ * by the attention.
+ *
+ * Page layout, for P = page_tokens, D = head_dim: for every kv head, key
+ * codes (P rows of D / 2 bytes), key scales (D / 32 rows of P fp16), then
+ * value codes and value scales alike. Eight consecutive channels share a
+ * little-endian dword, channel c in bits 4j .. 4j + 3, j = (c >> 1) + 4 (c & 1).
+ *
+ * Ragged batches, for the three calls below. Rows q_start[b] .. q_start[b + 1]
+ * - 1 of the activations (q_start: device, int32, n_seq + 1 ascending
+ * offsets) are the newest tokens of sequence b, n_b of them; lens[b] (device,
+ * int32) is the length of sequence b in the cache with them; its row i is at
+ * position lens[b] - n_b + i. q_start NULL: one row per sequence (row b, n_tok
+ * = n_seq). Rows outside every sequence (before q_start[0], from
+ * q_start[n_seq] on) are left as they were, and append and read do the same
+ * for a row whose position is negative or not below table_stride *
+ * page_tokens. Offsets that descend or leave 0 .. n_tok give that sequence no
+ * rows. These arrays live on the device
+ * and cannot be checked before the launch; whatever they hold, no call reads
+ * or writes outside the arrays it was given: a page number outside [0,
+ * n_pages) is never followed -- nothing is stored through it, reading gives
+ * NaN, and attention rows that see a key of it are NaN.
+ */
+typedef struct gq_kv4 {
+    void* pages;
+    int64_t n_pages;
+    int64_t page_tokens;
+    int64_t n_kv;
+    int64_t head_dim;
+    const int32_t* table;
+    int64_t table_stride;
+    int64_t n_seq;
+} gq_kv4;
+
+/* Bytes of a page: page_tokens * n_kv * head_dim * 9 / 8. Negative for a
+ * shape that gq_kv4 does not allow. Host only. */
+int64_t gq_kv4_page_bytes(int64_t page_tokens, int64_t n_kv, int64_t head_dim);
+
+/*
+ * Stores the keys and values of n_tok token rows at their positions: k normed
+ * with kw (NULL: no norm) and rotated at its own position (rope NULL: no
+ * rotation), v as it is. With q not NULL the same launch also norms (qw) and
+ * rotates n_head query heads into q_out, as gq_qk_rope does; q_out may be q
+ * with the same stride. Keys are rotated in fp64 and rounded only into their
+ * blocks. k, v: [n_tok, n_kv, head_dim] with strides k_stride, v_stride; q,
+ * q_out: [n_tok, n_head, head_dim]. Slots of the pages that no row lands on
+ * are left as they were. Two rows of one call landing on one slot (two
+ * sequences that share the page) leave a mixture of both there. GQ_ERR_OVERLAP
+ * where q_out or the pages overlap an input (interleaved rows of one buffer
+ * with equal strides do not). n_tok == 0 is a no-op. Asynchronous on `stream`.
+ */
+int gq_kv4_append(const gq_kv4* cache, const float* k, int64_t k_stride, const float* v, int64_t v_stride,
+                  int64_t n_tok, const int32_t* q_start, const int32_t* lens, const gq_rope* rope,
+                  const float* kw, const float* q, int64_t q_stride, int64_t n_head, const float* qw,
+                  float* q_out, int64_t q_out_stride, float eps, void* stream);
+
+/*
+ * The held values of n_tok token rows as fp32, bit for bit: K and V are
+ * [n_tok, n_kv, head_dim], contiguous; either may be NULL (not wanted). With
+ * n_b = lens[b] for every sequence this reads whole sequences. Asynchronous
+ * on `stream`.
+ */
+int gq_kv4_read(const gq_kv4* cache, int64_t n_tok, const int32_t* q_start, const int32_t* lens, float* K,
+                float* V, void* stream);
+
+/*
+ * Attention of n_head query heads over the cache; query head h reads kv head
+ * h / (n_head / n_kv) (n_head a multiple of n_kv). For the row at position p:
+ *   out[h] = sum_j w_j V_j / sum_j w_j,  w_j = exp(scale * q_h . K_j),
+ * over the keys j < lens[b] with j <= p if causal is not 0, and j > p - window
+ * if window > 0. A row that sees no key is 0. A key or value whose scale is
+ * not finite reaches the rows that see it and no others.
+ *
+ * max_q: at least every n_b (rows of a sequence past max_q are left as they
+ * were); max_len: at least every lens[b], at most table_stride * page_tokens
+ * (a length past max_len is taken as max_len, a negative one as 0).
+ * The two and the shapes choose the kernel and how far long sequences are
+ * split over workgroups; nothing is read back, so a captured call follows
+ * lengths that change between replays, up to max_len. Products take q and
+ * the softmax weights as pairs of fp16 numbers on the matrix cores, sums,
+ * maximum and total are fp32: the error is about that of fp32 arithmetic
+ * (2^-22 of each term of the two products). Repeated calls give the same
+ * bits.
+ *
+ * ws: gq_kv4_attn_ws_bytes(...) bytes of device memory, 16-byte aligned, that
+ * no other call in flight uses (two streams, or two graphs that may run at
+ * once, need one each); its contents need no preparation and mean nothing
+ * afterwards. NULL is allowed where that size is 0. q and out: [n_tok,
+ * n_head, head_dim] with strides in floats. GQ_ERR_SHAPE if ws_bytes is too
+ * small; GQ_ERR_OVERLAP if out or ws overlaps another argument. n_tok == 0 is
+ * a no-op. Asynchronous on `stream`.
+ */
+int64_t gq_kv4_attn_ws_bytes(const gq_kv4* cache, int64_t n_head, int64_t max_q, int64_t max_len);
+int gq_kv4_attn(const gq_kv4* cache, const float* q, int64_t q_stride, int64_t n_head, int64_t n_tok,
+                const int32_t* q_start, const int32_t* lens, int64_t max_q, int64_t max_len, float scale,
+                int causal, int64_t window, float* out, int64_t out_stride, void* ws, int64_t ws_bytes,
+                void* stream);
 
 #ifdef __cplusplus
 }
