@@ -73,7 +73,7 @@ int check_cache(const gq_kv4* cache, int64_t n_tok, const int32_t* q_start, cons
   if (!cache) return GQ_ERR_NULL;
   const int64_t pb = gq_kv4_page_bytes(cache->page_tokens, cache->n_kv, cache->head_dim);
   if (pb < 0) return GQ_ERR_SHAPE;
-  if (cache->n_pages < 0 || cache->n_pages > kMaxDim || cache->n_pages > INT64_MAX / 2 / pb) return GQ_ERR_SHAPE;
+  if (cache->n_pages < 1 || cache->n_pages > kMaxDim || cache->n_pages > INT64_MAX / 2 / pb) return GQ_ERR_SHAPE;
   if (cache->n_seq < 0 || cache->n_seq > kMaxDim || n_tok < 0 || n_tok > kMaxDim) return GQ_ERR_SHAPE;
   if (cache->table_stride < 0 || cache->table_stride > kMaxDim / cache->page_tokens) return GQ_ERR_SHAPE;
   if (!q_start && n_tok != cache->n_seq) return GQ_ERR_SHAPE;
@@ -95,7 +95,7 @@ int check_cache(const gq_kv4* cache, int64_t n_tok, const int32_t* q_start, cons
 }
 
 int check_cache_ptrs(const gq::Kv4Args& c) {
-  if ((!c.pages && c.n_pages > 0) || (!c.table && c.n_seq > 0 && c.table_stride > 0) || (!c.lens && c.n_seq > 0))
+  if (!c.pages || (!c.table && c.n_seq > 0 && c.table_stride > 0) || (!c.lens && c.n_seq > 0))
     return GQ_ERR_NULL;
   if ((uintptr_t)c.pages % 16 || (uintptr_t)c.table % 4 || (uintptr_t)c.lens % 4 || (uintptr_t)c.q_start % 4)
     return GQ_ERR_ALIGN;

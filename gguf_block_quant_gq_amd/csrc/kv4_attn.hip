@@ -1,13 +1,28 @@
 // kv4_attn.hip -- attention over the paged 4-bit key/value cache.
 //
 // Mathematics. For a query row, o = sum_j w_j v_j / sum_j w_j with w_j =
-// 2^(x_j - m), x_j = scale log2(e) q . k_j and m the running maximum: one pass
-// over the keys, the sums being multiplied by 2^(m_old - m_new) whenever the
-// maximum moves.
+// 2^(x_j - m), x_j = scale log2(e) q . k_j and m a running maximum: one pass
+// over the keys, the sums being multiplied by 2^(m_old - m_new) when the
+// maximum has moved by more than kSlack (until then the weights just grow past
+// 1, up to 2^kSlack, which fp16 holds).
 //
-// The plain kernel: a workgroup per row and query head; GL = head_dim / 8
-// lanes (rounded up to a power of two) hold 8 channels each, so a wave works
-// on 64 / GL keys at a time and the dot product is a lane reduction.
+// Exact operands. Both products run on the fp16 matrix cores. A held value d
+// (n - 8), d of 8 bits, is exact in fp16; q (scaled by a power of two so that
+// a row's largest magnitude lies in [2^9, 2^10)) and the weights are taken as
+// hi + lo, two fp16 numbers that carry 22 bits, and both parts are multiplied.
+// Products are exact, sums fp32. Taking only the hi parts would halve the
+// matrix work and cost 2^-12 per term, a thousand times fp32's own rounding.
+//
+// Dequantisation. A nibble n read as an fp8 (e4m3) byte is n 2^-9 for all 16
+// codes, so one v_cvt_scalef32_pk_f16_fp8 makes two codes fp16 and one packed
+// fma, n d - 8 d, the two values (8 d is a power of two times d, so the fma
+// rounds once, and not at all for scales of 8 bits): 11 instructions for the
+// 8 channels of a dword.
+//
+// Both products are computed transposed, S^T = K Q^T and O^T = V^T P^T: the
+// matrix cores leave a row's scores of several keys in one lane, in just the
+// places where the second product takes its weights, so the softmax needs no
+// data movement but the maximum over the lanes that share a row.
 #include <algorithm>
 
 #include "gq_device.h"
@@ -17,9 +32,16 @@ namespace gq {
 
 namespace {
 
-constexpr int kThreads = 256;
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// The keys that a row sees: lo .. hi - 1 (none: hi <= lo).
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr float kSlack = 6.f;
+constexpr int kTile = 32;  // keys that a wave of the row kernel takes at once
+
+// The keys that a row at position pos sees: lo .. hi - 1 (none: hi <= lo).
 struct Seen {
   int lo, hi;
 };
@@ -34,6 +56,465 @@ __device__ __forceinline__ Seen seen_keys(const AttnArgs& a, int pos, int len) {
 __device__ __forceinline__ int clamped_len(const AttnArgs& a, int len) {
   return len < 0 ? 0 : len > a.max_len ? a.max_len : len;
 }
+
+__device__ __forceinline__ h8 as_h8(h2 a, h2 b, h2 c, h2 d) {
+  const u32x4 v = {__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
+                   __builtin_bit_cast(uint32_t, d)};
+  return __builtin_bit_cast(h8, v);
+}
+
+// Codes in bytes 0, 1 (WORD = 0) or 2, 3 (1) of w, each a nibble, as values
+// n d + off; off = -8 d.
+template <int WORD>
+__device__ __forceinline__ h2 two_values(uint32_t w, h2 d, h2 off) {
+  const h2 n = __builtin_bit_cast(h2, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, kFp8CodeScale, WORD));
+  return __builtin_elementwise_fma(n, d, off);
+}
+
+// A scale (16 bits) in both halves.
+__device__ __forceinline__ h2 both(uint32_t bits) {
+  return __builtin_bit_cast(h2, bits | bits << 16);
+}
+
+__device__ __forceinline__ h2 minus8(h2 d) { return d * h2{(_Float16)-8.f, (_Float16)-8.f}; }
+
+// A dword of eight channels of one key as a matrix operand. Slots 0 .. 7 hold
+// channels 0, 4, 1, 5, 2, 6, 3, 7 (bytes hold even channels in their low
+// nibbles ...): the query operand is laid out alike.
+__device__ __forceinline__ h8 key_operand(uint32_t w, h2 d, h2 off) {
+  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+  return as_h8(two_values<0>(lo, d, off), two_values<1>(lo, d, off), two_values<0>(hi, d, off),
+               two_values<1>(hi, d, off));
+}
+__host__ __device__ constexpr int slot_channel(int j) { return (j >> 1) + 4 * (j & 1); }
+
+// The largest of a value over the four lanes l, l ^ 16, l ^ 32, l ^ 48, in all
+// of them; and the sum.
+__device__ __forceinline__ float max_over_rows(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  v = fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
+}
+
+__device__ __forceinline__ float sum_over_rows(float v) {
+  v += __shfl_xor(v, 32);
+  return v + __shfl_xor(v, 16);
+}
+
+// A query row's scaling: |q| * up has its largest magnitude in [2^9, 2^10),
+// and down takes the products back, the softmax scale included.
+struct RowScale {
+  float up, down;
+};
+
+__device__ __forceinline__ RowScale row_scale(float largest, float scale) {
+  const int e = (int)((__builtin_bit_cast(uint32_t, largest) >> 23) & 0xFF) - 127;
+  const int up = 9 - e > 127 ? 127 : 9 - e < -126 ? -126 : 9 - e;
+  RowScale r;
+  r.up = __builtin_copysignf(__builtin_bit_cast(float, (uint32_t)(up + 127) << 23), scale);
+  // never 0, so that a masked score of minus infinity stays one
+  r.down = fmaxf(__builtin_ldexpf(__builtin_fabsf(scale), -up), 1.17549435e-38f);
+  return r;
+}
+
+// ---------------------------------------------------------- the row kernel --
+// Few rows a sequence (single tokens, or a few, times the query heads that
+// share a kv head: at most 16). A wave takes 32 keys at a time on its own: its
+// lanes read their keys' codes and scales straight into the places where the
+// matrix operands need them, the next tile's loads in flight while this one
+// is computed, and no LDS is used until the waves' sums are added at the end.
+//   keys: lane (m, g) (l = 16 g + m) reads D / 4 channels of key m of each
+//   half tile: whole dwords of one or two blocks, so one scale each.
+//   values: lane (m, g) reads D / 16 channels, from channel m D / 16 on, of
+//   the eight keys whose weights it holds (4 g .. 4 g + 3 of each half tile).
+//   Pairs of keys are put side by side by two byte permutes; channel i of
+//   every lane makes matrix tile i.
+// FUSED: at most 8 rows. Columns 0 .. 7 of the query operand hold hi parts and
+// 8 .. 15 the lo parts of the same rows, so one product gives both, one lane
+// rotation adds them, and likewise for the weights.
+// Bound: HBM. 144 bytes a token and kv head of 128 channels against about
+// 1500 cycles of issue per 32 keys and SIMD, an issue limit near 7 TB/s.
+template <int D>
+struct RowTile {
+  static constexpr int KW = D / 32;             // dwords of a key per lane
+  static constexpr int KS = KW > 4 ? KW / 4 : 1;  // scales of a key per lane
+  static constexpr int VW = D >= 256 ? 2 : 1;   // dwords (D = 64: halves of one) of a value per lane
+  uint32_t k[2][KW];
+  uint32_t ks[2][KS];
+  uint32_t v[8][VW];
+  u32x2 vs[2];
+};
+
+template <int D, bool FUSED>
+__global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a) {
+  typedef RowTile<D> Tile;
+  constexpr int KW = Tile::KW, VW = Tile::VW, NT = D / 16;  // NT: matrix tiles of channels
+  constexpr int ROWS = FUSED ? 8 : 16;
+  constexpr int PASS = ROWS * D > 2048 ? ROWS * D / 2048 : 1;  // the waves' sums meet in 32 KB of LDS
+  constexpr int TP = NT / PASS;
+  __shared__ float so[kWaves][ROWS][TP * 16 + 4];
+  __shared__ float sm[kWaves][16], sl[kWaves][16];
+
+  const Kv4Args& c = a.c;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, g = lane >> 4;
+  const int kvh = blockIdx.x % c.n_kv, split = blockIdx.x / c.n_kv;
+  const int hd = c.hd, lg = c.page_log2, P = 1 << lg;
+  const int row = FUSED ? (m & 7) : m;
+
+  // lane constants: offsets inside a key part and a value part of a page
+  const int row_b = hd / 2;
+  const int kcol = g * (KW * 4) < row_b ? g * (KW * 4) : 0;
+  const int kblk = g * (KW * 8) / 32, vblk0 = m * NT / 32;
+  const bool v_on = m * NT < hd;
+  const int vcol = v_on ? m * (NT / 2) : 0, vblk = v_on ? vblk0 : 0;
+  const int koff = m * row_b + kcol;
+  const int voff = 4 * g * row_b + vcol;
+  const int scale_at = kv4_code_bytes(hd, lg);
+  const int64_t head_at = kv4_part(c, kvh, 0);
+  const int part_b = kv4_part_bytes(hd, lg);
+
+  for (int b = blockIdx.y; b < c.n_seq; b += gridDim.y) {
+    const SeqRows s = seq_rows(c, b);
+    const int n = s.n < a.max_q ? s.n : a.max_q;
+    const int R = n * a.group;
+    if (n <= 0) continue;
+    const int len = clamped_len(a, s.len);
+    // the first and last rows' keys bound everyone's
+    const int pos0 = len - s.n;
+    const Seen first = seen_keys(a, pos0, len), last = seen_keys(a, pos0 + n - 1, len);
+    const int t = s.first + row / a.group;
+    const Seen mine = seen_keys(a, pos0 + row / a.group, len);
+    const int lo = first.lo & ~(kTile - 1), hi = last.hi;
+    const int tiles = hi > first.lo ? (hi - lo + kTile - 1) / kTile : 0;
+    const int parts = a.splits * kWaves, mypart = split * kWaves + wave;
+    const int tile0 = (int)((int64_t)tiles * mypart / parts), tile1 = (int)((int64_t)tiles * (mypart + 1) / parts);
+
+    // the query operand: lane (m, g) holds the channels that its key lanes
+    // hold, of row m (FUSED: the hi part of row m, or the lo part of row m - 8)
+    h8 qh[KW], ql[FUSED ? 1 : KW];
+    float down;
+    {
+      const bool on = row < R;
+      const float* qr = a.q + (int64_t)(on ? t : s.first) * a.q_stride +
+                        (int64_t)(kvh * a.group + (on ? row % a.group : 0)) * hd;
+      float x[KW][8];
+      float big = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const int c0 = (g * KW + w) * 8;
+        const bool in = on && c0 < hd;
+        const f32x4 u = load_f32x4(qr + (in ? c0 : 0)), v = load_f32x4(qr + (in ? c0 + 4 : 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[w][i] = in ? u[i] : 0.f, x[w][i + 4] = in ? v[i] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = fmaxf(big, __builtin_fabsf(x[w][i]));
+      }
+      const RowScale rs = row_scale(max_over_rows(big), a.scale);
+      down = rs.down;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        h8 h, l;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float y = x[w][slot_channel(j)] * rs.up;
+          h[j] = (_Float16)y;
+          l[j] = (_Float16)(y - (float)h[j]);
+        }
+        if constexpr (FUSED) {
+          qh[w] = m < 8 ? h : l;
+        } else {
+          qh[w] = h;
+          ql[w] = l;
+        }
+      }
+    }
+
+    const int32_t* table = c.table + (int64_t)b * c.table_stride;
+    const auto page_id = [&](int key) { return table[(key < hi ? key : hi - 1) >> lg]; };
+    const auto load = [&](Tile& x, int key0, int id0, int id1) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int id = u ? id1 : id0;
+        const bool ok = id >= 0 && id < c.n_pages;
+        const int slot0 = (key0 + 16 * u) & (P - 1);
+        const uint8_t* kp = c.pages + (int64_t)(ok ? id : 0) * c.page_bytes + head_at;
+        const uint8_t* kc = kp + slot0 * row_b + koff;
+        if constexpr (KW == 2) {
+          u32x2 v;
+          __builtin_memcpy(&v, __builtin_assume_aligned(kc, 8), 8);
+          x.k[u][0] = v.x, x.k[u][1] = v.y;
+        } else {
+#pragma unroll
+          for (int w = 0; w < KW; w += 4) {
+            u32x4 v;
+            __builtin_memcpy(&v, __builtin_assume_aligned(kc + 4 * w, 16), 16);
+            x.k[u][w] = v.x, x.k[u][w + 1] = v.y, x.k[u][w + 2] = v.z, x.k[u][w + 3] = v.w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < Tile::KS; ++i) {
+          const bool in = (kblk + i) * 32 < hd;
+          const uint32_t d = load_u16(kp + scale_at + 2 * (((in ? kblk + i : 0) << lg) + slot0 + m));
+          x.ks[u][i] = ok ? (in ? d : 0u) : 0x7E00u;  // no page: NaN scores
+        }
+        const uint8_t* vc = kp + part_b + slot0 * row_b + voff;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (D == 64) {
+            x.v[4 * u + j][0] = load_u16(vc + j * row_b);
+          } else if constexpr (D == 128) {
+            x.v[4 * u + j][0] = load_u32(vc + j * row_b);
+          } else {
+            u32x2 v;
+            __builtin_memcpy(&v, __builtin_assume_aligned(vc + j * row_b, 8), 8);
+            x.v[4 * u + j][0] = v.x, x.v[4 * u + j][1] = v.y;
+          }
+        }
+        u32x2 d;
+        __builtin_memcpy(&d, __builtin_assume_aligned(kp + part_b + scale_at + 2 * ((vblk << lg) + slot0 + 4 * g), 8), 8);
+        x.vs[u] = ok && v_on ? d : u32x2{0u, 0u};
+      }
+    };
+
+    f32x4 o[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float mx = -INFINITY, l = 0.f;
+
+    const auto compute = [&](Tile& x, int key0) {
+      // scores: rows are this half tile's keys 4 g + r, columns query rows
+      f32x4 sc[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        sc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          const h2 d = both(x.ks[u][w / 4]);
+          const h8 k = key_operand(x.k[u][w], d, minus8(d));
+          sc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[w], sc[u], 0, 0, 0);
+          if constexpr (!FUSED) sc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[w], sc[u], 0, 0, 0);
+        }
+        if constexpr (FUSED) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sc[u][r] += dpp_f32<0x128>(sc[u][r]);  // row_ror:8: hi + lo
+        }
+      }
+      // masks, in tiles that reach past some row's keys. There a value whose
+      // scale is not finite must not meet the zero weight of a row that does
+      // not see it: it is taken as 0, and its key's scores as NaN for the
+      // rows that do. Elsewhere it reaches every row by itself.
+      if (key0 + kTile > first.hi || key0 < last.lo) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t bits = (x.vs[u][r >> 1] >> (16 * (r & 1))) & 0xFFFF;
+            const bool out = key0 + 16 * u + 4 * g + r >= hi;
+            const bool inf = (bits & 0x7C00) == 0x7C00;
+            const uint64_t any = __ballot(inf && !out);
+            if ((any >> (16 * g)) & 0xFFFF) bad |= 1u << (4 * u + r);
+            if (inf || out) x.vs[u][r >> 1] &= r & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int key = key0 + 16 * u + 4 * g + r;
+            if (bad >> (4 * u + r) & 1) sc[u][r] = __builtin_nanf("");
+            if (key < mine.lo || key >= mine.hi) sc[u][r] = -INFINITY;
+          }
+        }
+      }
+      float top = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
+                        fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
+      top = max_over_rows(top) * down;
+      if (__any(top > mx + kSlack)) {
+        const float nm = fmaxf(mx, top);
+        const float f = __builtin_amdgcn_exp2f(mx - (nm == -INFINITY ? 0.f : nm));
+        mx = nm;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) o[i] *= f;
+      }
+      const float base = mx == -INFINITY ? 0.f : mx;
+      const float part = FUSED && m < 8 ? 0.f : -1.f;
+      h2 ph[4], pl[4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+          const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][r], down, -base));
+          const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][r + 1], down, -base));
+          l += p0 + p1;
+          const h2 h = {(_Float16)p0, (_Float16)p1};
+          // the lo part (FUSED: p itself in the hi columns)
+          const float r0 = __builtin_fmaf((float)h.x, part, p0), r1 = __builtin_fmaf((float)h.y, part, p1);
+          ph[2 * u + r / 2] = h;
+          pl[2 * u + r / 2] = h2{(_Float16)r0, (_Float16)r1};
+        }
+      }
+      const h8 wl = as_h8(pl[0], pl[1], pl[2], pl[3]);
+      const h8 wh = as_h8(ph[0], ph[1], ph[2], ph[3]);
+      // values: pairs of keys side by side, channel by channel
+      h2 vd[4], voffs[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        vd[p] = __builtin_bit_cast(h2, (uint32_t)x.vs[p >> 1][p & 1]);
+        voffs[p] = minus8(vd[p]);
+      }
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+#pragma unroll
+        for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
+          // bytes (2 half) and (2 half + 1) of the pairs' dwords, interleaved
+          uint32_t lo4[4], hi4[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const uint32_t y = __builtin_amdgcn_perm(x.v[2 * p + 1][w], x.v[2 * p][w], half ? 0x07030602u : 0x05010400u);
+            lo4[p] = y & 0x0F0F0F0Fu;
+            hi4[p] = (y >> 4) & 0x0F0F0F0Fu;
+          }
+          // D = 64: the lane's channels are every second one; else even
+          // channels lie in the low half of a dword, odd ones in the high
+          const auto tile = [&](int i, h8 v) {
+            const int at = D == 64 ? i : w * 8 + 2 * i + half;
+            o[at] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, wl, o[at], 0, 0, 0);
+            if constexpr (!FUSED) o[at] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, wh, o[at], 0, 0, 0);
+          };
+          tile(0, as_h8(two_values<0>(lo4[0], vd[0], voffs[0]), two_values<0>(lo4[1], vd[1], voffs[1]),
+                        two_values<0>(lo4[2], vd[2], voffs[2]), two_values<0>(lo4[3], vd[3], voffs[3])));
+          tile(1, as_h8(two_values<0>(hi4[0], vd[0], voffs[0]), two_values<0>(hi4[1], vd[1], voffs[1]),
+                        two_values<0>(hi4[2], vd[2], voffs[2]), two_values<0>(hi4[3], vd[3], voffs[3])));
+          tile(2, as_h8(two_values<1>(lo4[0], vd[0], voffs[0]), two_values<1>(lo4[1], vd[1], voffs[1]),
+                        two_values<1>(lo4[2], vd[2], voffs[2]), two_values<1>(lo4[3], vd[3], voffs[3])));
+          tile(3, as_h8(two_values<1>(hi4[0], vd[0], voffs[0]), two_values<1>(hi4[1], vd[1], voffs[1]),
+                        two_values<1>(hi4[2], vd[2], voffs[2]), two_values<1>(hi4[3], vd[3], voffs[3])));
+        }
+      }
+    };
+
+    if (tile0 < tile1) {
+      Tile x0, x1;
+      int key = lo + tile0 * kTile;
+      const int end = lo + tile1 * kTile;
+      load(x0, key, page_id(key), page_id(key + 16));
+      // page numbers run two tiles ahead of the compute, data one
+      int id0 = page_id(key + kTile), id1 = page_id(key + kTile + 16);
+      for (; key < end; key += 2 * kTile) {
+        int jd0 = page_id(key + 2 * kTile), jd1 = page_id(key + 2 * kTile + 16);
+        if (key + kTile < end) load(x1, key + kTile, id0, id1);
+        compute(x0, key);
+        if (key + kTile >= end) break;
+        id0 = page_id(key + 3 * kTile), id1 = page_id(key + 3 * kTile + 16);
+        if (key + 2 * kTile < end) load(x0, key + 2 * kTile, jd0, jd1);
+        compute(x1, key + kTile);
+      }
+    }
+    l = sum_over_rows(l);
+
+    // the waves' sums, in wave order
+    if (g == 0) sm[wave][m] = mx, sl[wave][m] = l;
+    __syncthreads();
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm[w][m]);
+    const float f = __builtin_amdgcn_exp2f(mx - (M == -INFINITY ? 0.f : M));
+    const int64_t slot0 = (((int64_t)b * c.n_kv + kvh) * a.splits + split) * ((int64_t)a.max_q * a.group);
+    float* ml = a.part + (int64_t)c.n_seq * c.n_kv * a.splits * a.max_q * a.group * hd;
+    for (int p = 0; p < PASS; ++p) {
+      if (p) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        if (i / TP == p) {
+          f32x4 v = o[i];
+          if constexpr (FUSED) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] += dpp_f32<0x128>(v[r]);
+          }
+          v *= f;
+          if (!FUSED || m < 8) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) so[wave][row][(4 * g + r) * TP + i % TP] = v[r];
+          }
+        }
+      }
+      __syncthreads();
+      for (int e = threadIdx.x; e < R * TP * 16; e += kThreads) {
+        const int r = e / (TP * 16), q = e % (TP * 16);
+        // place q: lane row q / TP, tile p TP + q % TP
+        const int qm = q / TP, i = p * TP + q % TP;
+        const int ch = D == 64 ? 8 * (qm >> 1) + (qm & 1) + 2 * i : qm * NT + i;
+        if (ch >= hd) continue;
+        float RM = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) RM = fmaxf(RM, sm[w][r]);
+        const float rb = RM == -INFINITY ? 0.f : RM;
+        float sum = 0.f, tot = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          sum += so[w][r][q];
+          tot += sl[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - rb);
+        }
+        if (a.splits == 1) {
+          a.out[(int64_t)(s.first + r / a.group) * a.out_stride + (int64_t)(kvh * a.group + r % a.group) * hd + ch] =
+              tot == 0.f ? 0.f : sum / tot;
+        } else {
+          a.part[(slot0 + r) * hd + ch] = sum;
+          if (ch == 0) ml[2 * (slot0 + r)] = RM, ml[2 * (slot0 + r) + 1] = tot;
+        }
+      }
+    }
+    __syncthreads();  // before the next sequence writes sm, sl
+  }
+}
+
+// The parts of a split row added up: a wave per row, the maxima and totals
+// first. Parts without keys have a maximum of minus infinity.
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
+  const Kv4Args& c = a.c;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t per = (int64_t)a.max_q * a.group, heads = (int64_t)c.n_seq * c.n_kv, rows = heads * per;
+  const float* ml = a.part + rows * a.splits * c.hd;
+  for (int64_t i = (int64_t)blockIdx.x * kWaves + wave; i < rows; i += (int64_t)gridDim.x * kWaves) {
+    const int64_t bh = i / per;
+    const int r = (int)(i - bh * per), b = (int)(bh / c.n_kv), kvh = (int)(bh - (int64_t)b * c.n_kv);
+    const SeqRows s = seq_rows(c, b);
+    if (r / a.group >= s.n) continue;
+    const int64_t slot0 = bh * a.splits * per + r;
+    float M = -INFINITY;
+    for (int p = lane; p < a.splits; p += 64) M = fmaxf(M, ml[2 * (slot0 + p * per)]);
+#pragma unroll
+    for (int w = 32; w > 0; w /= 2) M = fmaxf(M, __shfl_xor(M, w));
+    const float base = M == -INFINITY ? 0.f : M;
+    float tot = 0.f, sum[4] = {};
+    for (int p = 0; p < a.splits; ++p) {
+      const float pm = ml[2 * (slot0 + p * per)];
+      if (pm == -INFINITY && ml[2 * (slot0 + p * per) + 1] == 0.f) continue;
+      const float f = __builtin_amdgcn_exp2f(pm - base);
+      tot += f * ml[2 * (slot0 + p * per) + 1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int ch = lane + 64 * e;
+        if (ch < c.hd) sum[e] += f * a.part[(slot0 + p * per) * c.hd + ch];
+      }
+    }
+    float* out = a.out + (int64_t)(s.first + r / a.group) * a.out_stride + (int64_t)(kvh * a.group + r % a.group) * c.hd;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int ch = lane + 64 * e;
+      if (ch < c.hd) out[ch] = tot == 0.f ? 0.f : sum[e] / tot;
+    }
+  }
+}
+
+// --------------------------------------------------------- the plain kernel --
+// A workgroup per row and query head; GL = head_dim / 8 lanes (rounded up to
+// a power of two) hold 8 channels each, so a wave works on 64 / GL keys at a
+// time and the dot product is a lane reduction.
 
 // 8 channels of one key or value: d (n - 8).
 __device__ __forceinline__ void load8(const Kv4Args& c, const uint8_t* part, int slot, int sub, float x[8]) {
@@ -122,11 +603,41 @@ __global__ __launch_bounds__(kThreads) void attn_plain_kernel(AttnArgs a) {
   }
 }
 
+// Rows of a sequence and kv head up to which the row kernel is taken.
+constexpr int kRowKernelRows = 16;
+
+template <int D>
+void launch_rows(const AttnArgs& a, bool fused, hipStream_t s) {
+  const int64_t gx = (int64_t)a.c.n_kv * a.splits;
+  const dim3 grid((unsigned)gx, (unsigned)std::max<int64_t>(1, std::min<int64_t>(a.c.n_seq, (1 << 22) / gx)));
+  if (fused) hipLaunchKernelGGL((attn_rows_kernel<D, true>), grid, dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((attn_rows_kernel<D, false>), grid, dim3(kThreads), 0, s, a);
+}
+
 }  // namespace
 
-int kv4_attn_splits(int64_t, int64_t, int64_t, int64_t) { return 1; }
+// Parts that a sequence's keys are cut into: enough workgroups to fill the
+// GPU (four per CU), none with less than 256 keys.
+int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len) {
+  if (rows > kRowKernelRows || n_seq <= 0) return 1;
+  const int64_t want = 1024 / std::max<int64_t>(1, n_seq * n_kv), most = (max_len + 255) / 256;
+  return (int)std::max<int64_t>(1, std::min(want, most));
+}
 
 hipError_t launch_kv4_attn(const AttnArgs& a, hipStream_t s) {
+  const int64_t rows = (int64_t)a.max_q * a.group;
+  if (rows <= kRowKernelRows) {
+    const bool fused = rows <= 8;
+    if (a.c.hd <= 64) launch_rows<64>(a, fused, s);
+    else if (a.c.hd <= 128) launch_rows<128>(a, fused, s);
+    else launch_rows<256>(a, fused, s);
+    if (a.splits > 1) {
+      const int64_t all = a.c.n_seq * (int64_t)a.c.n_kv * rows;
+      const int64_t wgs = std::min<int64_t>((all + kWaves - 1) / kWaves, 1 << 20);
+      hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)wgs), dim3(kThreads), 0, s, a);
+    }
+    return hipGetLastError();
+  }
   const int gl = a.c.hd <= 32 ? 4 : a.c.hd <= 64 ? 8 : a.c.hd <= 128 ? 16 : 32;
   const dim3 grid(std::min(a.c.n_tok, 1 << 20), a.n_head), block(kThreads);
   if (gl == 4) hipLaunchKernelGGL((attn_plain_kernel<4>), grid, block, 0, s, a);

@@ -490,8 +490,8 @@ int gq_qk_rope(const float* x, int64_t x_stride, int64_t n_tok, int64_t n_head, 
                int64_t out_stride, void* stream);
 
 /*
- * gq_kv4: a paged key/value cache in 4-bit blocks. pages: n_pages pages of
- * gq_kv4_page_bytes bytes (16-byte aligned); page_tokens: tokens a page
+ * gq_kv4: a paged key/value cache in 4-bit blocks. pages: n_pages (1 or more)
+ * pages of gq_kv4_page_bytes bytes (16-byte aligned); page_tokens: tokens a page
  * holds, a power of two from 16 to 1024; n_kv: key/value heads; head_dim: a
  * multiple of 32 from 32 to 256. table (device, int32, [n_seq, table_stride]):
  * entry (b, i) is the page that holds the tokens i * page_tokens .. of

@@ -85,7 +85,7 @@ def test_qk_rope_arguments(lib):
 
 def test_append_arguments(lib):
     S, N, AL, OV = gq.GQ_ERR_SHAPE, gq.GQ_ERR_NULL, gq.GQ_ERR_ALIGN, gq.GQ_ERR_OVERLAP
-    for bad in (kv4(n_pages=-1), kv4(n_pages=1 << 31), kv4(page_tokens=20), kv4(head_dim=80), kv4(n_kv=0),
+    for bad in (kv4(n_pages=-1), kv4(n_pages=0), kv4(n_pages=1 << 31), kv4(page_tokens=20), kv4(head_dim=80), kv4(n_kv=0),
                 kv4(table_stride=-1), kv4(table_stride=(1 << 26) + 1), kv4(n_seq=-1)):
         for call in (append, read, attn):
             assert call(lib, c=bad) == S
@@ -143,6 +143,23 @@ def test_attention_arguments(lib):
     for bad in (dict(out=A[2]), dict(out=A[2] + 256), dict(out=A[0]), dict(out=A[1]), dict(out=A[5]), dict(out=A[6])):
         assert attn(lib, **bad) == OV, bad
     assert attn(lib, max_q=0) == gq.GQ_OK
+
+
+def test_attention_workspace(lib):
+    # a long context of one sequence is split; its workspace is asked for
+    c = kv4(table_stride=1024, n_seq=1)
+    need = lib.gq_kv4_attn_ws_bytes(ctypes.addressof(c), 4, 1, 16384)
+    assert need > 0
+    args = dict(c=c, start=None, n=1, max_q=1, max_len=16384)
+    assert attn(lib, **args, wsb=need - 1) == gq.GQ_ERR_SHAPE
+    assert attn(lib, **args, ws=None) == gq.GQ_ERR_NULL
+    assert attn(lib, **args, ws=A[4] + 8) == gq.GQ_ERR_ALIGN
+    for o in (A[0], A[1], A[2], A[3], A[6]):
+        assert attn(lib, **args, ws=o) == gq.GQ_ERR_OVERLAP
+    for bad in (dict(h=3), dict(max_q=-1), dict(max_len=16385)):
+        a = dict(h=4, max_q=1, max_len=16384) | bad
+        assert lib.gq_kv4_attn_ws_bytes(ctypes.addressof(c), a["h"], a["max_q"], a["max_len"]) < 0
+    assert lib.gq_kv4_attn_ws_bytes(None, 4, 1, 16) < 0
 
 
 def test_python_binding_refuses_cpu_tensors():
