@@ -34,6 +34,7 @@ namespace {
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
@@ -472,6 +473,360 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a) {
   }
 }
 
+// --------------------------------------------------------- the tile kernel --
+// Many rows a sequence (prompts and their chunks). A workgroup owns 128 rows
+// of one kv head -- consecutive tokens times the query heads that share it, 32
+// rows a wave -- and walks the keys 64 at a time (32 for heads past 128
+// channels). The tile is dequantised once into LDS as fp16 by all four waves
+// (waves 0, 1 the keys, 2, 3 the values), two tiles deep: the next tile's
+// codes are in flight while this one is computed, and one barrier a tile is
+// enough.
+//   LDS: keys [key][channel], values [channel][key], in 16-byte chunks whose
+//   place in the row is xored with the row, so that the 16 lanes that read
+//   (or write) one chunk column at a time cover all 64 banks.
+//   S^T (32 keys x 32 rows per matrix instruction) leaves a row's scores in
+//   the lanes l and l ^ 32; the weights go straight into the second product,
+//   whose keys are ordered as the scores lie (chunk 2 t + h of a value row
+//   holds keys 16 t + 4 h + 0 .. 3 and 16 t + 8 + 4 h + 0 .. 3).
+// Bound: issue. Per wave and 64 keys of 128 channels, 128 matrix instructions
+// (about 37 cycles each, which do not overlap vector instructions on this
+// GPU) and about 600 vector ones for softmax and dequantisation.
+template <int D>
+struct TileCfg {
+  static constexpr int KT = D > 128 ? 32 : 64;        // keys per tile
+  static constexpr int KPT = KT * D / 32 / 128;       // key blocks staged per thread (waves 0, 1)
+  static constexpr int VTASKS = KT / 8 * (D / 8);     // value tasks (waves 2, 3): 8 keys x 8 channels
+  static constexpr int CH = D / 8;                    // chunks of a key row
+  static constexpr int VCH = KT / 8;                  // chunks of a value row
+  static_assert(VTASKS <= 128, "one value task per thread");
+};
+
+template <int D>
+__device__ __forceinline__ int key_chunk(int key, int c) {
+  const int x = D == 64 ? (key >> 1) & 7 : key & 15;
+  return key * (D / 8) + (c ^ x);
+}
+
+template <int D>
+__device__ __forceinline__ int value_chunk(int row, int c) {
+  constexpr int VCH = TileCfg<D>::VCH;
+  const int x = VCH == 8 ? (row >> 1) & 7 : (row >> 2) & 3;
+  return row * VCH + (c ^ x);
+}
+
+constexpr int kTileRows = 128;
+
+template <int D>
+__global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(AttnArgs a) {
+  typedef TileCfg<D> C;
+  constexpr int KT = C::KT, KB = KT / 32, NT = D / 32, KS = D / 16;
+  __shared__ h8 kbuf[2][KT * D / 8];
+  __shared__ h8 vbuf[2][KT * D / 8];
+  __shared__ unsigned long long bad[3];  // keys of a masked tile whose value has a scale that is not finite
+
+  const Kv4Args& c = a.c;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int m = lane & 31, h = lane >> 5;
+  // kv heads fastest: neighbours in the grid go to different XCDs, so each
+  // XCD's L2 holds few heads. Later rows see more keys and start first.
+  const int kvh = blockIdx.x % c.n_kv, rest = blockIdx.x / c.n_kv;
+  const int split = rest % a.splits, row_tiles = gridDim.x / c.n_kv / a.splits;
+  const int row0 = (row_tiles - 1 - rest / a.splits) * kTileRows;
+  const int hd = c.hd, lg = c.page_log2, P = 1 << lg, row_b = hd / 2;
+  const int scale_at = kv4_code_bytes(hd, lg), part_b = kv4_part_bytes(hd, lg);
+  const int64_t head_at = kv4_part(c, kvh, 0);
+
+  for (int b = blockIdx.y; b < c.n_seq; b += gridDim.y) {
+    const SeqRows s = seq_rows(c, b);
+    const int n = s.n < a.max_q ? s.n : a.max_q;
+    const int R = n * a.group;
+    if (row0 >= R) continue;
+    const int len = clamped_len(a, s.len), pos0 = len - s.n;
+    const int rlast = (row0 + kTileRows < R ? row0 + kTileRows : R) - 1;
+    const Seen first = seen_keys(a, pos0 + row0 / a.group, len), last = seen_keys(a, pos0 + rlast / a.group, len);
+    const int lo = first.lo & ~(KT - 1), hi = last.hi;
+    const int tiles = hi > first.lo ? (hi - lo + KT - 1) / KT : 0;
+    const int tile0 = (int)((int64_t)tiles * split / a.splits), tile1 = (int)((int64_t)tiles * (split + 1) / a.splits);
+    const int32_t* table = c.table + (int64_t)b * c.table_stride;
+
+    const int row = row0 + wave * 32 + m;
+    const bool row_on = row < R;
+    const int tok = row_on ? row / a.group : 0;
+    const int head = kvh * a.group + (row_on ? row - tok * a.group : 0);
+    const Seen mine = seen_keys(a, pos0 + tok, len);
+
+    // staging: what this thread brings in of each tile
+    const bool key_side = wave < 2;
+    const int st = tid & 127;
+    const bool value_on = !key_side && st < C::VTASKS;
+    const int vcol = st % (D / 8), vchunk = st / (D / 8);
+    const int vkey = 16 * (vchunk >> 1) + 4 * (vchunk & 1);  // and 8 further on
+    const bool vin = vcol * 8 < hd;
+    u32x4 raw[C::KPT > 2 ? C::KPT : 2];
+    uint32_t rawd[4];
+    int ids[C::KPT];
+
+    const auto find = [&](int tile) {  // page numbers of a tile's tasks
+#pragma unroll
+      for (int i = 0; i < C::KPT; ++i) {
+        const int key = lo + tile * KT + (key_side ? (st + 128 * i) / (D / 32) : vkey);
+        if (key_side || i == 0) ids[i] = table[(key < hi ? key : hi - 1) >> lg];
+      }
+    };
+    const auto fetch = [&](int tile) {
+      if (key_side) {
+#pragma unroll
+        for (int i = 0; i < C::KPT; ++i) {
+          const int id = st + 128 * i, blk = id % (D / 32), slot = (lo + tile * KT + id / (D / 32)) & (P - 1);
+          const bool ok = ids[i] >= 0 && ids[i] < c.n_pages, in = blk * 32 < hd;
+          const uint8_t* kp = c.pages + (int64_t)(ok ? ids[i] : 0) * c.page_bytes + head_at;
+          __builtin_memcpy(&raw[i], __builtin_assume_aligned(kp + slot * row_b + (in ? blk : 0) * 16, 16), 16);
+          const uint32_t d = load_u16(kp + scale_at + 2 * (((in ? blk : 0) << lg) + slot));
+          rawd[i] = ok ? (in ? d : 0u) : 0x7E00u;
+        }
+      } else if (value_on) {
+        const int slot = (lo + tile * KT + vkey) & (P - 1);
+        const bool ok = ids[0] >= 0 && ids[0] < c.n_pages;
+        const uint8_t* vp = c.pages + (int64_t)(ok ? ids[0] : 0) * c.page_bytes + head_at + part_b;
+        const uint8_t* vc = vp + slot * row_b + (vin ? vcol : 0) * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          raw[0][j] = load_u32(vc + j * row_b);
+          raw[1][j] = load_u32(vc + (8 + j) * row_b);
+        }
+        const uint8_t* vs = vp + scale_at + 2 * (((vin ? vcol / 4 : 0) << lg) + slot);
+        u32x2 d0, d1;
+        __builtin_memcpy(&d0, __builtin_assume_aligned(vs, 8), 8);
+        __builtin_memcpy(&d1, __builtin_assume_aligned(vs + 16, 8), 8);
+        const bool on = ok && vin;
+        rawd[0] = on ? d0.x : 0u, rawd[1] = on ? d0.y : 0u, rawd[2] = on ? d1.x : 0u, rawd[3] = on ? d1.y : 0u;
+      }
+    };
+    const auto masked = [&](int tile) {
+      const int key0 = lo + tile * KT;
+      return key0 + KT > first.hi || key0 < last.lo;
+    };
+    const auto stage = [&](int tile) {
+      const int buf = tile & 1;
+      if (tid == 0 && masked(tile + 1)) bad[(tile + 1) % 3] = 0;
+      if (key_side) {
+#pragma unroll
+        for (int i = 0; i < C::KPT; ++i) {
+          const int id = st + 128 * i, blk = id % (D / 32), key = id / (D / 32);
+          const h2 d = both(rawd[i]), off = minus8(d);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) kbuf[buf][key_chunk<D>(key, blk * 4 + w)] = key_operand(raw[i][w], d, off);
+        }
+      } else if (value_on) {
+        if (masked(tile)) {
+          const int key0 = lo + tile * KT + vkey;
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            const int k = (p < 4 ? 0 : 4) + p;  // 0 .. 3, 8 .. 11
+            const uint32_t bits = (rawd[p >> 1] >> (16 * (p & 1))) & 0xFFFF;
+            const bool out = key0 + k >= hi, inf = (bits & 0x7C00) == 0x7C00;
+            if (inf && !out) atomicOr(&bad[tile % 3], 1ull << (vkey + k));
+            if (inf || out) rawd[p >> 1] &= p & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+          }
+        }
+        h2 d[4], off[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) d[p] = __builtin_bit_cast(h2, rawd[p]), off[p] = minus8(d[p]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t lo4[4], hi4[4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const uint32_t y = __builtin_amdgcn_perm(raw[p >> 1][2 * (p & 1) + 1], raw[p >> 1][2 * (p & 1)],
+                                                     half ? 0x07030602u : 0x05010400u);
+            lo4[p] = y & 0x0F0F0F0Fu;
+            hi4[p] = (y >> 4) & 0x0F0F0F0Fu;
+          }
+          const auto put = [&](int i, h8 v) {  // channel 2 i + half of the dword
+            vbuf[buf][value_chunk<D>((2 * i + half) * (D / 8) + vcol, vchunk)] = v;
+          };
+          put(0, as_h8(two_values<0>(lo4[0], d[0], off[0]), two_values<0>(lo4[1], d[1], off[1]),
+                       two_values<0>(lo4[2], d[2], off[2]), two_values<0>(lo4[3], d[3], off[3])));
+          put(1, as_h8(two_values<0>(hi4[0], d[0], off[0]), two_values<0>(hi4[1], d[1], off[1]),
+                       two_values<0>(hi4[2], d[2], off[2]), two_values<0>(hi4[3], d[3], off[3])));
+          put(2, as_h8(two_values<1>(lo4[0], d[0], off[0]), two_values<1>(lo4[1], d[1], off[1]),
+                       two_values<1>(lo4[2], d[2], off[2]), two_values<1>(lo4[3], d[3], off[3])));
+          put(3, as_h8(two_values<1>(hi4[0], d[0], off[0]), two_values<1>(hi4[1], d[1], off[1]),
+                       two_values<1>(hi4[2], d[2], off[2]), two_values<1>(hi4[3], d[3], off[3])));
+        }
+      }
+    };
+
+    if (tid < 3) bad[tid] = 0;
+    if (tile0 < tile1) {
+      find(tile0);
+      fetch(tile0);
+      if (tile0 + 1 < tile1) find(tile0 + 1);
+    }
+
+    // the query operand, hi and lo parts
+    h8 qh[KS], ql[KS];
+    float down;
+    {
+      const float* qr = a.q + (int64_t)(s.first + tok) * a.q_stride + (int64_t)head * hd;
+      float big = 0.f;
+#pragma unroll
+      for (int w = 0; w < KS; ++w) {
+        const int c0 = 16 * w + 8 * h;
+        const bool in = row_on && c0 < hd;
+        const f32x4 u = load_f32x4(qr + (in ? c0 : 0)), v = load_f32x4(qr + (in ? c0 + 4 : 4));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) big = fmaxf(big, in ? fmaxf(__builtin_fabsf(u[i]), __builtin_fabsf(v[i])) : 0.f);
+      }
+      const RowScale rs = row_scale(fmaxf(big, __shfl_xor(big, 32)), a.scale);
+      down = rs.down;
+#pragma unroll
+      for (int w = 0; w < KS; ++w) {
+        const int c0 = 16 * w + 8 * h;
+        const bool in = row_on && c0 < hd;
+        const f32x4 u = load_f32x4(qr + (in ? c0 : 0)), v = load_f32x4(qr + (in ? c0 + 4 : 4));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int e = slot_channel(j);
+          const float y = in ? (e < 4 ? u[e & 3] : v[e & 3]) * rs.up : 0.f;
+          qh[w][j] = (_Float16)y;
+          ql[w][j] = (_Float16)(y - (float)qh[w][j]);
+        }
+      }
+    }
+
+    f32x16 o[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
+    float mx = -INFINITY, l = 0.f;
+
+    __syncthreads();  // bad is clear
+    if (tile0 < tile1) {
+      stage(tile0);
+      if (tile0 + 1 < tile1) fetch(tile0 + 1);
+      if (tile0 + 2 < tile1) find(tile0 + 2);
+    }
+    __syncthreads();
+    for (int tile = tile0; tile < tile1; ++tile) {
+      const int buf = tile & 1, key0 = lo + tile * KT;
+      f32x16 sc[KB];
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sc[k][r] = 0.f;
+#pragma unroll
+        for (int w = 0; w < KS; ++w) {
+          const h8 x = kbuf[buf][key_chunk<D>(32 * k + m, 2 * w + h)];
+          sc[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, qh[w], sc[k], 0, 0, 0);
+          sc[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, ql[w], sc[k], 0, 0, 0);
+        }
+      }
+      if (masked(tile)) {
+        const unsigned long long bm = bad[tile % 3];
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int at = 32 * k + 8 * (r >> 2) + 4 * h + (r & 3), key = key0 + at;
+            if (bm >> at & 1) sc[k][r] = __builtin_nanf("");
+            if (key < mine.lo || key >= mine.hi) sc[k][r] = -INFINITY;
+          }
+        }
+      }
+      float top = sc[0][0];
+#pragma unroll
+      for (int k = 0; k < KB; ++k)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[k][r]);
+      {
+        const uint32_t u = __builtin_bit_cast(uint32_t, top);
+        const auto both_halves = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        top = fmaxf(__builtin_bit_cast(float, (uint32_t)both_halves[0]),
+                    __builtin_bit_cast(float, (uint32_t)both_halves[1])) * down;
+      }
+      if (__any(top > mx + kSlack)) {
+        const float nm = fmaxf(mx, top);
+        const float f = __builtin_amdgcn_exp2f(mx - (nm == -INFINITY ? 0.f : nm));
+        mx = nm;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) o[i] *= f;
+      }
+      const float base = mx == -INFINITY ? 0.f : mx;
+      h8 ph[2 * KB], pl[2 * KB];
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          h2 hs[4], ls[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[k][8 * t + 2 * r], down, -base));
+            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[k][8 * t + 2 * r + 1], down, -base));
+            l += p0 + p1;
+            hs[r] = h2{(_Float16)p0, (_Float16)p1};
+            ls[r] = h2{(_Float16)(p0 - (float)hs[r].x), (_Float16)(p1 - (float)hs[r].y)};
+          }
+          ph[2 * k + t] = as_h8(hs[0], hs[1], hs[2], hs[3]);
+          pl[2 * k + t] = as_h8(ls[0], ls[1], ls[2], ls[3]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+#pragma unroll
+        for (int t = 0; t < 2 * KB; ++t) {
+          const h8 x = vbuf[buf][value_chunk<D>(32 * i + m, 2 * t + h)];
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, ph[t], o[i], 0, 0, 0);
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, pl[t], o[i], 0, 0, 0);
+        }
+      }
+      if (tile + 1 < tile1) {
+        stage(tile + 1);
+        if (tile + 2 < tile1) fetch(tile + 2);
+        if (tile + 3 < tile1) find(tile + 3);
+      }
+      __syncthreads();
+    }
+
+    l += __shfl_xor(l, 32);
+    if (row_on) {
+      const int64_t slot = ((((int64_t)b * c.n_kv + kvh) * a.splits + split) * a.max_q) * a.group + row;
+      float* out;
+      float f = 1.f;
+      if (a.splits == 1) {
+        out = a.out + (int64_t)(s.first + tok) * a.out_stride + (int64_t)head * hd;
+        f = l == 0.f ? 0.f : 1.f / l;
+      } else {
+        out = a.part + slot * hd;
+        float* ml = a.part + (int64_t)c.n_seq * c.n_kv * a.splits * a.max_q * a.group * hd + 2 * slot;
+        if (h == 0) ml[0] = mx, ml[1] = l;
+      }
+      // value row r of matrix tile i is channel (32 i + r) / (D / 8) of dword
+      // (32 i + r) % (D / 8): a lane holds all 8 channels of D / 16 dwords
+      constexpr int W = D / 8, RUNS = D / 16;
+#pragma unroll
+      for (int e = 0; e < RUNS; ++e) {
+        // rows with r & 3 = e & 3, and (r >> 2) = e >> 2 modulo W / 8
+        float x[8];
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const int r0 = ch * W + 8 * (e >> 2) + (e & 3);  // without 4 h
+          x[ch] = o[r0 / 32][4 * ((r0 % 32) / 8) + (e & 3)] * f;
+        }
+        const int w = 8 * (e >> 2) + 4 * h + (e & 3);
+        if (w * 8 < hd) {
+          const f32x4 u = {x[0], x[1], x[2], x[3]}, v = {x[4], x[5], x[6], x[7]};
+          __builtin_memcpy(__builtin_assume_aligned(out + w * 8, 4), &u, 16);
+          __builtin_memcpy(__builtin_assume_aligned(out + w * 8 + 4, 4), &v, 16);
+        }
+      }
+    }
+    __syncthreads();  // before the next sequence clears bad
+  }
+}
+
 // The parts of a split row added up: a wave per row, the maxima and totals
 // first. Parts without keys have a maximum of minus infinity.
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
@@ -511,98 +866,6 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
   }
 }
 
-// --------------------------------------------------------- the plain kernel --
-// A workgroup per row and query head; GL = head_dim / 8 lanes (rounded up to
-// a power of two) hold 8 channels each, so a wave works on 64 / GL keys at a
-// time and the dot product is a lane reduction.
-
-// 8 channels of one key or value: d (n - 8).
-__device__ __forceinline__ void load8(const Kv4Args& c, const uint8_t* part, int slot, int sub, float x[8]) {
-  const uint32_t code = load_u32(part + slot * (c.hd / 2) + sub * 4);
-  const float d = half_bits_to_float(
-      load_u16(part + kv4_code_bytes(c.hd, c.page_log2) + 2 * (((sub >> 2) << c.page_log2) + slot)));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = d * (float)((int)(code >> (4 * ((i >> 1) + 4 * (i & 1))) & 15) - 8);
-}
-
-template <int GL>
-__global__ __launch_bounds__(kThreads) void attn_plain_kernel(AttnArgs a) {
-  constexpr int kKeys = kThreads / GL;  // keys in flight
-  __shared__ float sm[kKeys], sl[kKeys], so[kKeys][GL * 8 + 1];
-  const int tid = threadIdx.x, sub = tid % GL, g = tid / GL;
-  const Kv4Args& c = a.c;
-  const int h = blockIdx.y, kvh = h / a.group;
-  const bool on = sub * 8 < c.hd;
-  const int cl = on ? sub : 0;
-  for (int b = 0, t = blockIdx.x; t < c.n_tok; t += gridDim.x) {
-    // the row's sequence
-    SeqRows s{0, 0, 0};
-    if (c.q_start) {
-      int lo = 0, hi = c.n_seq;
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (c.q_start[mid + 1] <= t) lo = mid + 1;
-        else hi = mid;
-      }
-      b = lo;
-    } else {
-      b = t;
-    }
-    if (b >= c.n_seq) continue;
-    s = seq_rows(c, b);
-    const int64_t i = (int64_t)t - s.first;
-    if (i < 0 || i >= s.n || i >= a.max_q) continue;
-    const int len = clamped_len(a, s.len);
-    const Seen k = seen_keys(a, len - s.n + (int)i, len);
-    const float* q = a.q + t * a.q_stride + (int64_t)h * c.hd;
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = on ? q[sub * 8 + e] * a.scale : 0.f;
-    float m = -INFINITY, l = 0.f, o[8] = {};
-    for (int j = k.lo + g; j < k.hi; j += kKeys) {
-      const uint8_t* page = page_of(c, b, j);
-      const int slot = j & ((1 << c.page_log2) - 1);
-      float kx[8], vx[8];
-      if (page) {
-        load8(c, page + kv4_part(c, kvh, 0), slot, cl, kx);
-        load8(c, page + kv4_part(c, kvh, 1), slot, cl, vx);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) kx[e] = vx[e] = __builtin_nanf("");
-      }
-      float d = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) d = __builtin_fmaf(x[e], kx[e], d);
-      if (!on) d = 0.f;
-#pragma unroll
-      for (int w = GL / 2; w > 0; w /= 2) d += __shfl_xor(d, w, GL);
-      const float mn = fmaxf(m, d), base = mn == -INFINITY ? 0.f : mn;
-      const float r = exp2f(m - base), p = exp2f(d - base);
-      l = l * r + p;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = o[e] * r + p * vx[e];
-      m = mn;
-    }
-    __syncthreads();
-    if (sub == 0) sm[g] = m, sl[g] = l;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) so[g][sub * 8 + e] = o[e];
-    __syncthreads();
-    float mx = -INFINITY;
-    for (int e = 0; e < kKeys; ++e) mx = fmaxf(mx, sm[e]);
-    if (mx == -INFINITY) mx = 0.f;
-    for (int ch = tid; ch < c.hd; ch += kThreads) {
-      float lt = 0.f, ot = 0.f;
-      for (int e = 0; e < kKeys; ++e) {
-        const float r = exp2f(sm[e] - mx);
-        lt += r * sl[e];
-        ot += r * so[e][ch];
-      }
-      a.out[t * a.out_stride + (int64_t)h * c.hd + ch] = k.hi > k.lo ? ot / lt : 0.f;
-    }
-  }
-}
-
 // Rows of a sequence and kv head up to which the row kernel is taken.
 constexpr int kRowKernelRows = 16;
 
@@ -614,14 +877,24 @@ void launch_rows(const AttnArgs& a, bool fused, hipStream_t s) {
   else hipLaunchKernelGGL((attn_rows_kernel<D, false>), grid, dim3(kThreads), 0, s, a);
 }
 
+template <int D>
+void launch_tiles(const AttnArgs& a, hipStream_t s) {
+  const int64_t rows = (int64_t)a.max_q * a.group;
+  const int64_t gx = (int64_t)a.c.n_kv * a.splits * ((rows + kTileRows - 1) / kTileRows);
+  const dim3 grid((unsigned)gx, (unsigned)std::max<int64_t>(1, std::min<int64_t>(a.c.n_seq, (1 << 22) / gx)));
+  hipLaunchKernelGGL((attn_tile_kernel<D>), grid, dim3(kThreads), 0, s, a);
+}
+
 }  // namespace
 
 // Parts that a sequence's keys are cut into: enough workgroups to fill the
-// GPU (four per CU), none with less than 256 keys.
+// GPU (four per CU for the row kernel, two for the tile kernel), none with
+// less than 256 keys.
 int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len) {
-  if (rows > kRowKernelRows || n_seq <= 0) return 1;
-  const int64_t want = 1024 / std::max<int64_t>(1, n_seq * n_kv), most = (max_len + 255) / 256;
-  return (int)std::max<int64_t>(1, std::min(want, most));
+  if (n_seq <= 0 || rows <= 0) return 1;
+  const int64_t tiles = rows <= kRowKernelRows ? 1 : (rows + kTileRows - 1) / kTileRows;
+  const int64_t want = (rows <= kRowKernelRows ? 1024 : 512) / std::max<int64_t>(1, n_seq * n_kv * tiles);
+  return (int)std::max<int64_t>(1, std::min(want, (max_len + 255) / 256));
 }
 
 hipError_t launch_kv4_attn(const AttnArgs& a, hipStream_t s) {
@@ -631,19 +904,16 @@ hipError_t launch_kv4_attn(const AttnArgs& a, hipStream_t s) {
     if (a.c.hd <= 64) launch_rows<64>(a, fused, s);
     else if (a.c.hd <= 128) launch_rows<128>(a, fused, s);
     else launch_rows<256>(a, fused, s);
-    if (a.splits > 1) {
-      const int64_t all = a.c.n_seq * (int64_t)a.c.n_kv * rows;
-      const int64_t wgs = std::min<int64_t>((all + kWaves - 1) / kWaves, 1 << 20);
-      hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)wgs), dim3(kThreads), 0, s, a);
-    }
-    return hipGetLastError();
+  } else {
+    if (a.c.hd <= 64) launch_tiles<64>(a, s);
+    else if (a.c.hd <= 128) launch_tiles<128>(a, s);
+    else launch_tiles<256>(a, s);
   }
-  const int gl = a.c.hd <= 32 ? 4 : a.c.hd <= 64 ? 8 : a.c.hd <= 128 ? 16 : 32;
-  const dim3 grid(std::min(a.c.n_tok, 1 << 20), a.n_head), block(kThreads);
-  if (gl == 4) hipLaunchKernelGGL((attn_plain_kernel<4>), grid, block, 0, s, a);
-  else if (gl == 8) hipLaunchKernelGGL((attn_plain_kernel<8>), grid, block, 0, s, a);
-  else if (gl == 16) hipLaunchKernelGGL((attn_plain_kernel<16>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((attn_plain_kernel<32>), grid, block, 0, s, a);
+  if (a.splits > 1) {
+    const int64_t all = a.c.n_seq * (int64_t)a.c.n_kv * rows;
+    const int64_t wgs = std::min<int64_t>((all + kWaves - 1) / kWaves, 1 << 20);
+    hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)wgs), dim3(kThreads), 0, s, a);
+  }
   return hipGetLastError();
 }
 
