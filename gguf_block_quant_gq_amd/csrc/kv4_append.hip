@@ -16,9 +16,10 @@
 // Split. hd / 8 lanes (rounded up to a power of two) own a head, 8 channels
 // each; a wave holds whole heads, so the norm's sum and the block's largest
 // value are lane exchanges, and a head may be turned in place (its loads all
-// precede its stores). A workgroup takes one token at a time: its sines and
-// cosines (about 60 fp64 operations a pair) are computed once into LDS and
-// kept in registers over the token's heads.
+// precede its stores). A workgroup takes a token, or four where there are many:
+// their sines and cosines (about 60 fp64 operations a pair) are computed once
+// into LDS for all heads, with the first heads' loads in flight; from then on
+// the next pass's loads run under each pass's arithmetic.
 #include <algorithm>
 
 #include "gq_device.h"
@@ -100,20 +101,58 @@ __device__ __forceinline__ double block_scale(double a) {
   return r > 8160.0 ? 8160.0 : r < -8160.0 ? -8160.0 : r;
 }
 
-// rint(x / d), ties to even, clamped to -8 .. 7. x times 1/d may be off by a
-// few units of 2^-52, enough to miss an exact tie: the remainder x - r d is
-// exact, and is compared with d / 2.
-__device__ __forceinline__ int block_code(double x, double d, double inv) {
-  double t = x * inv;
-  t = t < -8.0 ? -8.0 : t > 7.0 ? 7.0 : t;  // a NaN passes both tests and ends as code 0
-  double r = __builtin_rint(t);
-  const double rem = __builtin_fma(-r, d, x);  // in units of d: x / d - r
-  const double twice = 2.0 * __builtin_fabs(rem), ad = __builtin_fabs(d);
-  const double side = (rem < 0) == (d < 0) ? 1.0 : -1.0;
-  const bool odd = ((int)r & 1) != 0;
-  if (twice > ad || (twice == ad && odd)) r += side;
-  r = r < -8.0 ? -8.0 : r > 7.0 ? 7.0 : r;
-  return (int)r;
+// rint(x / d), ties to even, clamped to -8 .. 7. The quotient is taken in
+// fp32, which may fall on the wrong side of a tie; the remainder x - r d is
+// exact in fp64 and is compared with |d| / 2.
+__device__ __forceinline__ int block_code(double x, double d, float inv, double half_d) {
+  const float r = __builtin_rintf(__builtin_amdgcn_fmed3f((float)x * inv, -8.f, 7.f));
+  const double rem = __builtin_fma(-(double)r, d, x);
+  const int n = (int)r;
+  const int side = ((int)((__builtin_bit_cast(uint64_t, rem) ^ __builtin_bit_cast(uint64_t, d)) >> 32) >> 31) | 1;
+  const bool over = __builtin_fabs(rem) > half_d, tie = __builtin_fabs(rem) == half_d;
+  const int c = n + (((int)over | ((int)tie & n)) & 1 ? side : 0);
+  return c < -8 ? -8 : c > 7 ? 7 : c;
+}
+
+// 1 / sqrt(v): the hardware's estimate and two Newton steps (an infinite v,
+// whose steps would be NaN, gives 0).
+__device__ __forceinline__ double inv_sqrt(double v) {
+  double r = __builtin_amdgcn_rsq(v);
+  const double hv = 0.5 * v;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) r = __builtin_fma(r, __builtin_fma(-hv * r, r, 0.5), r);
+  return v == __builtin_inf() ? 0.0 : r;
+}
+
+// The value of largest magnitude of a block, which four lanes hold eight
+// channels each of: the first of equals, a NaN before everything. The signed
+// extremes decide it unless they are equal in magnitude; then (and for NaN)
+// the channels are gone through in order.
+__device__ __forceinline__ double block_largest(const double y[8]) {
+  double top = y[0], bot = y[0];
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) nan |= __builtin_isunordered(y[i], y[i + 1]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) top = __builtin_fmax(top, y[i]), bot = __builtin_fmin(bot, y[i]);
+  top = __builtin_fmax(top, dpp_f64<0xB1>(top)), bot = __builtin_fmin(bot, dpp_f64<0xB1>(bot));
+  top = __builtin_fmax(top, dpp_f64<0x4E>(top)), bot = __builtin_fmin(bot, dpp_f64<0x4E>(bot));
+  double a = top > -bot ? top : bot;
+  if (__any(nan | (top == -bot))) {
+    double best = y[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      const bool take = (best == best) & !(__builtin_fabs(y[i]) <= __builtin_fabs(best));
+      best = take ? y[i] : best;
+    }
+    const double o1 = dpp_f64<0xB1>(best);  // the lower lane of a pair wins a tie
+    bool tie = __builtin_fabs(o1) == __builtin_fabs(best) && (threadIdx.x & 1);
+    best = (best == best) & (!(__builtin_fabs(o1) <= __builtin_fabs(best)) | tie) ? o1 : best;
+    const double o2 = dpp_f64<0x4E>(best);
+    tie = __builtin_fabs(o2) == __builtin_fabs(best) && (threadIdx.x & 2);
+    a = (best == best) & (!(__builtin_fabs(o2) <= __builtin_fabs(best)) | tie) ? o2 : best;
+  }
+  return a;
 }
 
 struct QkArgs {
@@ -124,155 +163,163 @@ struct QkArgs {
   int n_tok;
   int hd;
   float eps;
+  double inv_hd;
 };
 
-// GL lanes per head. FAST: whole groups of 8 channels turn with a whole group
-// (rot a multiple of 16, or of 8 with interleaved pairs), so partners are one
-// more 32-byte load.
-template <int GL, bool APPEND, bool FAST>
+// GL lanes per head, TOK tokens per workgroup. FAST: whole groups of 8
+// channels turn with a whole group (rot a multiple of 16, or of 8 with
+// interleaved pairs), so partners are one more 32-byte load. APART: half
+// layout.
+template <int GL, int TOK, bool APPEND, bool APART, bool FAST>
 __global__ __launch_bounds__(kThreads) void qk_rope_kernel(QkArgs a) {
-  __shared__ f64x2 turn[kMaxPairs];
+  __shared__ f64x2 turn[TOK][kMaxPairs];
+  __shared__ uint8_t* pages[TOK];
+  __shared__ int where[TOK];           // positions; -1: the row belongs to none
   constexpr int kHeads = kThreads / GL;  // heads per pass
   const int tid = threadIdx.x, sub = tid % GL, slot = tid / GL;
   const int hd = a.hd, c0 = sub * 8, half = a.r.half;
   const bool lane_on = c0 < hd;
+  const int cl = lane_on ? c0 : 0;
   const int heads = a.part[0].n_head + (APPEND ? a.part[1].n_head + a.part[2].n_head : 0);
 
   // this lane's partners: channel c turns with c + half, or with c - half
   // (half layout), or with its neighbour (interleaved)
   const bool low = c0 < half, rot_on = lane_on && c0 < 2 * half;
-  const int pc0 = a.r.interleaved || !rot_on ? c0 : low ? c0 + half : c0 - half;
+  const auto partner = [&](int c) { return c < half ? c + half : c < 2 * half ? c - half : c; };
+  const int pc0 = rot_on ? (low ? c0 + half : c0 - half) : cl;
 
-  for (int t = blockIdx.x; t < a.n_tok; t += gridDim.x) {
-    int seq = 0, pos = 0;
-    if constexpr (APPEND) {
-      pos = row_position(a.c, t, &seq);
-      if (pos < 0) continue;  // the same for the whole workgroup
-    } else {
-      pos = half > 0 ? a.pos[t] : 0;
-    }
-    __syncthreads();  // the pass before has read its turns
-    for (int p = tid; p < half; p += kThreads) {
-      const f64x2 sc = sin_cos((double)pos * (double)a.r.freqs[p]);
-      turn[p] = sc * (double)a.r.mscale;
-    }
-    __syncthreads();
-    uint8_t* page = nullptr;
-    if constexpr (APPEND) page = page_of(a.c, seq, pos);
-
+  for (int t0 = blockIdx.x * TOK; t0 < a.n_tok; t0 += gridDim.x * TOK) {
+    const int toks = a.n_tok - t0 < TOK ? a.n_tok - t0 : TOK;
+    bool first = true;
     for (int h0 = blockIdx.y * kHeads; h0 < heads; h0 += gridDim.y * kHeads) {
+      // a head for this group of lanes, in all tokens of the workgroup
       int h = h0 + slot, kind = 0;
+      const bool head_on = h < heads;
+      h = head_on ? h : 0;
       if constexpr (APPEND) {
         if (h >= a.part[0].n_head) h -= a.part[0].n_head, kind = 1;
         if (kind == 1 && h >= a.part[1].n_head) h -= a.part[1].n_head, kind = 2;
       }
-      const HeadArgs& ha = APPEND ? a.part[kind] : a.part[0];
-      const bool on = lane_on && h0 + slot < heads;
-      const bool turns = on && rot_on && kind != 2;
-      const float* xh = ha.x + t * ha.x_stride + (int64_t)(on ? h : 0) * hd;
-      double y[8], z[8];  // this lane's channels and their partners
-      const int cl = lane_on ? c0 : 0;
-      {
-        const f32x4 u = load_f32x4(xh + cl), v = load_f32x4(xh + cl + 4);
+      const HeadArgs ha = a.part[APPEND ? kind : 0];
+      const float* xh = ha.x + t0 * ha.x_stride + (int64_t)h * hd;
+      const bool rotates = half > 0 && (!APPEND || kind != 2);
+      f32x4 x[TOK][2], z[APART ? TOK : 1][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = on ? u[i] : 0.f, y[i + 4] = on ? v[i] : 0.f;
-      }
-      if (turns && !a.r.interleaved) {
-        if constexpr (FAST) {
-          const f32x4 u = load_f32x4(xh + pc0), v = load_f32x4(xh + pc0 + 4);
+      for (int k = 0; k < TOK; ++k) {
+        const float* p = xh + (k < toks ? k : 0) * ha.x_stride;
+        x[k][0] = load_f32x4(p + cl), x[k][1] = load_f32x4(p + cl + 4);
+        if (APART && rotates) {
+          if constexpr (FAST) {
+            z[k][0] = load_f32x4(p + pc0), z[k][1] = load_f32x4(p + pc0 + 4);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] = u[i], z[i + 4] = v[i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int c = c0 + i;
-            z[i] = xh[c < half ? c + half : c < 2 * half ? c - half : c];
+            for (int i = 0; i < 8; ++i) z[k][i >> 2][i & 3] = p[partner(cl + i)];
           }
         }
       }
-      const float* w = ha.w;
-      if (w && kind != 2) {
-        double ss = 0.0;
+      const bool normed = ha.w && (!APPEND || kind != 2);
+      f32x4 w[2] = {{1.f, 1.f, 1.f, 1.f}, {1.f, 1.f, 1.f, 1.f}}, wz[2] = {{1.f, 1.f, 1.f, 1.f}, {1.f, 1.f, 1.f, 1.f}};
+      if (normed) {
+        w[0] = load_f32x4(ha.w + cl), w[1] = load_f32x4(ha.w + cl + 4);
+        if (APART && rotates) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = __builtin_fma(y[i], y[i], ss);
-        ss = group_sum_f64<GL>(ss);
-        const double rs = 1.0 / __builtin_sqrt(ss / hd + (double)a.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i] *= rs * (double)w[cl + i];
-          if (turns && !a.r.interleaved) {
-            const int c = c0 + i;
-            z[i] *= rs * (double)w[FAST ? pc0 + i : c < half ? c + half : c < 2 * half ? c - half : c];
-          }
+          for (int i = 0; i < 8; ++i) wz[i >> 2][i & 3] = ha.w[FAST ? pc0 + i : partner(cl + i)];
         }
       }
-      if (turns) {
-        if (a.r.interleaved) {
+      if (first) {  // the angles, with the loads above in flight
+        first = false;
+        __syncthreads();  // the tokens before have been turned
+        if constexpr (APPEND) {
+          for (int k = tid >> 6; k < toks; k += kThreads / 64) {
+            int seq = 0;
+            const int p = row_position(a.c, t0 + k, &seq);
+            if ((tid & 63) == 0) where[k] = p, pages[k] = p < 0 ? nullptr : page_of(a.c, seq, p);
+          }
+          __syncthreads();
+        }
+        for (int i = tid; i < TOK * half; i += kThreads) {
+          const int k = TOK == 1 ? 0 : i / half, p = i - k * half;
+          if (k < toks) {
+            const int pos = APPEND ? where[k] : a.pos[t0 + k];
+            turn[k][p] = sin_cos((double)pos * (double)a.r.freqs[p]) * (double)a.r.mscale;
+          }
+        }
+        __syncthreads();
+      }
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const int p = (c0 + i) >> 1;
-            if (FAST || p < half) {
-              const f64x2 sc = turn[p];
-              const double u = y[i], v = y[i + 1];
-              y[i] = u * sc.y - v * sc.x;
-              y[i + 1] = v * sc.y + u * sc.x;
+      for (int k = 0; k < TOK; ++k) {
+        const int pos = APPEND && k < toks ? where[k] : 0;
+        const bool on = lane_on && head_on && k < toks && pos >= 0;
+        double y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = (double)(lane_on ? x[k][i >> 2][i & 3] : 0.f);
+        double rs = 1.0;
+        if (normed) {
+          double ss = 0.0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss = __builtin_fma(y[i], y[i], ss);
+          rs = inv_sqrt(__builtin_fma(group_sum_f64<GL>(ss), a.inv_hd, (double)a.eps));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] *= (double)w[i >> 2][i & 3];
+        }
+        if (rotates && rot_on) {
+          const f64x2* tn = turn[k];
+          if constexpr (APART) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int c = c0 + i;
+              const bool lo = FAST ? low : c < half;
+              double zi = (double)z[k][i >> 2][i & 3];
+              if (normed) zi *= (double)wz[i >> 2][i & 3];
+              if (FAST || c < 2 * half) {
+                const f64x2 sc = tn[lo ? c : c - half];
+                y[i] = __builtin_fma(y[i], sc.y, zi * (lo ? -sc.x : sc.x));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const int p = (c0 + i) >> 1;
+              if (FAST || p < half) {
+                const f64x2 sc = tn[p];
+                const double u = y[i], v = y[i + 1];
+                y[i] = __builtin_fma(u, sc.y, -(v * sc.x));
+                y[i + 1] = __builtin_fma(v, sc.y, u * sc.x);
+              }
             }
           }
-        } else {
+        }
+        if (normed) {  // the head's norm last: the rotation is linear
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int c = c0 + i;
-            const bool lo = FAST ? low : c < half;
-            if (FAST || c < 2 * half) {
-              const f64x2 sc = turn[lo ? c : c - half];
-              y[i] = lo ? y[i] * sc.y - z[i] * sc.x : y[i] * sc.y + z[i] * sc.x;
-            }
+          for (int i = 0; i < 8; ++i) y[i] *= rs;
+        }
+        if (!APPEND || kind == 0) {
+          if (on) {
+            float* o = ha.out + (t0 + k) * ha.out_stride + (int64_t)h * hd + c0;
+            const f32x4 u = {(float)y[0], (float)y[1], (float)y[2], (float)y[3]};
+            const f32x4 v = {(float)y[4], (float)y[5], (float)y[6], (float)y[7]};
+            __builtin_memcpy(__builtin_assume_aligned(o, 4), &u, 16);
+            __builtin_memcpy(__builtin_assume_aligned(o + 4, 4), &v, 16);
           }
-        }
-      }
-      if (!APPEND || kind == 0) {
-        if (on) {
-          float* o = ha.out + t * ha.out_stride + (int64_t)h * hd + c0;
-          const f32x4 u = {(float)y[0], (float)y[1], (float)y[2], (float)y[3]};
-          const f32x4 v = {(float)y[4], (float)y[5], (float)y[6], (float)y[7]};
-          __builtin_memcpy(__builtin_assume_aligned(o, 4), &u, 16);
-          __builtin_memcpy(__builtin_assume_aligned(o + 4, 4), &v, 16);
-        }
-      } else {
-        // the block's value of largest magnitude: the lowest channel among
-        // equals, a NaN before everything (four lanes share a block)
-        double best = y[0];
+        } else {
+          const double d = block_scale(block_largest(y));
+          const float inv = 1.f / (float)d;
+          const double half_d = 0.5 * __builtin_fabs(d);
+          uint32_t word = 0;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) {
-          const bool take = best == best && !(__builtin_fabs(y[i]) <= __builtin_fabs(best));
-          best = take ? y[i] : best;
-        }
-        {
-          const double o1 = dpp_f64<0xB1>(best);
-          const bool up = (tid & 1) != 0;  // the lower lane wins a tie
-          bool take = !(__builtin_fabs(o1) <= __builtin_fabs(best)) || (up && __builtin_fabs(o1) == __builtin_fabs(best));
-          best = best == best && take ? o1 : best;
-          const double o2 = dpp_f64<0x4E>(best);
-          const bool up2 = (tid & 2) != 0;
-          take = !(__builtin_fabs(o2) <= __builtin_fabs(best)) || (up2 && __builtin_fabs(o2) == __builtin_fabs(best));
-          best = best == best && take ? o2 : best;
-        }
-        const double d = block_scale(best);
-        const double inv = d != 0.0 ? 1.0 / d : 0.0;
-        uint32_t word = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t n = d != 0.0 && d == d ? (uint32_t)(block_code(y[i], d, inv) + 8) : 8u;
-          word |= n << (4 * ((i >> 1) + 4 * (i & 1)));
-        }
-        if (on && page) {
-          const int s = pos & ((1 << a.c.page_log2) - 1);
-          uint8_t* part = page + kv4_part(a.c, h, kind - 1);
-          *reinterpret_cast<uint32_t*>(part + s * (hd / 2) + sub * 4) = word;
-          if (sub % 4 == 0) {
-            const _Float16 d16 = (_Float16)(float)d;
-            _Float16* scales = reinterpret_cast<_Float16*>(part + kv4_code_bytes(hd, a.c.page_log2));
-            scales[((sub / 4) << a.c.page_log2) + s] = d16;
+          for (int i = 0; i < 8; ++i)
+            word |= (uint32_t)(block_code(y[i], d, inv, half_d) + 8) << (4 * ((i >> 1) + 4 * (i & 1)));
+          if (!(half_d > 0.0)) word = 0x88888888u;  // 0 or NaN
+          uint8_t* page = on ? pages[k] : nullptr;
+          if (page) {
+            const int s = pos & ((1 << a.c.page_log2) - 1);
+            uint8_t* part = page + kv4_part(a.c, h, kind - 1);
+            *reinterpret_cast<uint32_t*>(part + s * (hd / 2) + sub * 4) = word;
+            if (sub % 4 == 0) {
+              const _Float16 d16 = (_Float16)(float)d;
+              _Float16* scales = reinterpret_cast<_Float16*>(part + kv4_code_bytes(hd, a.c.page_log2));
+              scales[((sub / 4) << a.c.page_log2) + s] = d16;
+            }
           }
         }
       }
@@ -280,61 +327,89 @@ __global__ __launch_bounds__(kThreads) void qk_rope_kernel(QkArgs a) {
   }
 }
 
-// K and V of the token rows: a thread expands one dword of codes.
+// K and V of the token rows: a thread expands half a dword, four channels, so
+// that a wave stores whole kilobytes. TOK rows per workgroup share the look-up
+// of their pages (a chain of three loads that a row alone would wait for).
+template <int TOK>
 __global__ __launch_bounds__(kThreads) void kv4_read_kernel(Kv4Args c, float* __restrict__ K, float* __restrict__ V) {
-  const int words = c.hd / 8, per_row = 2 * c.n_kv * words;
-  for (int t = blockIdx.x; t < c.n_tok; t += gridDim.x) {
-    int seq = 0;
-    const int pos = row_position(c, t, &seq);
-    if (pos < 0) continue;
-    const uint8_t* page = page_of(c, seq, pos);
-    const int s = pos & ((1 << c.page_log2) - 1);
-    for (int i = blockIdx.y * kThreads + threadIdx.x; i < per_row; i += gridDim.y * kThreads) {
-      const int kv = i >= c.n_kv * words, j = i - kv * c.n_kv * words;
-      const int h = j / words, w = j - h * words;
-      float* out = kv ? V : K;
+  constexpr int STEP = TOK < 8 ? TOK : 8;
+  __shared__ const uint8_t* pages[TOK];
+  __shared__ int where[TOK];
+  const int tid = threadIdx.x, quads = c.hd / 4, per_row = 2 * c.n_kv * quads;
+  for (int t0 = blockIdx.x * TOK; t0 < c.n_tok; t0 += gridDim.x * TOK) {
+    const int toks = c.n_tok - t0 < TOK ? c.n_tok - t0 : TOK;
+    __syncthreads();
+    for (int k = tid >> 6; k < TOK; k += kThreads / 64) {
+      int seq = 0;
+      const int p = k < toks ? row_position(c, t0 + k, &seq) : -1;
+      if ((tid & 63) == 0) where[k] = p, pages[k] = p < 0 ? nullptr : page_of(c, seq, p);
+    }
+    __syncthreads();
+    // j: a quad of a head's key or value; the same for all rows
+    for (int j = blockIdx.y * kThreads + tid; j < per_row; j += gridDim.y * kThreads) {
+      const int part_i = j / quads, quad = j - part_i * quads;  // 2 head + (value)
+      float* out = part_i & 1 ? V : K;
       if (!out) continue;
-      f32x4 u, v;
-      if (page) {
-        const uint8_t* part = page + kv4_part(c, h, kv);
-        const uint32_t code = load_u32(part + s * (c.hd / 2) + w * 4);
-        const float d = half_bits_to_float(
-            load_u16(part + kv4_code_bytes(c.hd, c.page_log2) + 2 * (((w >> 2) << c.page_log2) + s)));
+      out += ((int64_t)t0 * c.n_kv + (part_i >> 1)) * c.hd + quad * 4;
+      const int64_t at = (int64_t)part_i * kv4_part_bytes(c.hd, c.page_log2);
+      const int code_at = (quad >> 1) * 4, scale_at = kv4_code_bytes(c.hd, c.page_log2) + 2 * ((quad >> 3) << c.page_log2);
+      const int shift = 8 * (quad & 1);  // channels 4 .. 7 lie two nibbles further up
+      for (int k0 = 0; k0 < toks; k0 += STEP) {
+        uint32_t code[STEP], d[STEP];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          u[b] = d * (float)((int)(code >> (4 * ((b >> 1) + 4 * (b & 1))) & 15) - 8);
-          v[b] = d * (float)((int)(code >> (4 * (2 + (b >> 1) + 4 * (b & 1))) & 15) - 8);
+        for (int k = 0; k < STEP; ++k) {  // STEP rows' loads in flight
+          const uint8_t* page = pages[k0 + k] ? pages[k0 + k] : c.pages;
+          const int s = where[k0 + k] & ((1 << c.page_log2) - 1);
+          code[k] = load_u32(page + at + s * (c.hd / 2) + code_at) >> shift;
+          d[k] = load_u16(page + at + scale_at + 2 * s);
         }
-      } else {
-        u = v = f32x4{__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
+#pragma unroll
+        for (int k = 0; k < STEP; ++k) {
+          if (where[k0 + k] < 0) continue;
+          const float f = pages[k0 + k] ? half_bits_to_float(d[k]) : __builtin_nanf("");
+          const uint32_t n = code[k];
+          const f32x4 u = {f * (float)((int)(n & 15) - 8), f * (float)((int)(n >> 16 & 15) - 8),
+                           f * (float)((int)(n >> 4 & 15) - 8), f * (float)((int)(n >> 20 & 15) - 8)};
+          __builtin_memcpy(__builtin_assume_aligned(out + (int64_t)(k0 + k) * c.n_kv * c.hd, 4), &u, 16);
+        }
       }
-      float* o = out + ((int64_t)t * c.n_kv + h) * c.hd + w * 8;
-      __builtin_memcpy(__builtin_assume_aligned(o, 4), &u, 16);
-      __builtin_memcpy(__builtin_assume_aligned(o + 4, 4), &v, 16);
     }
   }
+}
+
+// Token rows from which workgroups take several rows each. Fewer rows get a
+// workgroup per pass over the heads of one row, each with its own angles: the
+// call's latency counts then, and the GPU is not full.
+constexpr int kManyRows = 1024;
+
+template <int GL, bool APPEND, bool APART, bool FAST>
+void launch_qk_as(const QkArgs& a, int heads, hipStream_t s) {
+  if (a.n_tok >= kManyRows) {
+    constexpr int TOK = 4;
+    const int gx = std::min((a.n_tok + TOK - 1) / TOK, 1 << 20);
+    hipLaunchKernelGGL((qk_rope_kernel<GL, TOK, APPEND, APART, FAST>), dim3(gx), dim3(kThreads), 0, s, a);
+  } else {
+    const int passes = (heads * GL + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL((qk_rope_kernel<GL, 1, APPEND, APART, FAST>), dim3(a.n_tok, std::min(passes, 4096)),
+                       dim3(kThreads), 0, s, a);
+  }
+}
+
+template <int GL, bool APPEND>
+void launch_qk_gl(const QkArgs& a, int heads, hipStream_t s) {
+  const bool fast = a.r.half == 0 || (a.r.interleaved ? a.r.half % 4 == 0 : a.r.half % 8 == 0);
+  if (a.r.interleaved || a.r.half == 0)
+    fast ? launch_qk_as<GL, APPEND, false, true>(a, heads, s) : launch_qk_as<GL, APPEND, false, false>(a, heads, s);
+  else
+    fast ? launch_qk_as<GL, APPEND, true, true>(a, heads, s) : launch_qk_as<GL, APPEND, true, false>(a, heads, s);
 }
 
 template <bool APPEND>
 hipError_t launch_qk(const QkArgs& a, int heads, hipStream_t s) {
-  const int gl = a.hd <= 32 ? 4 : a.hd <= 64 ? 8 : a.hd <= 128 ? 16 : 32;
-  const int passes = (heads * gl + kThreads - 1) / kThreads;
-  // few tokens: a workgroup per pass over the heads, each with its own turns
-  // (latency counts); many: one workgroup per token computes them once
-  const int gy = a.n_tok >= 1024 ? 1 : std::min(passes, 65535);
-  const int gx = std::min(a.n_tok, 1 << 20);
-  const bool fast = a.r.half == 0 || (a.r.interleaved ? a.r.half % 4 == 0 : a.r.half % 8 == 0);
-  const dim3 grid(gx, gy), block(kThreads);
-#define GQ_QK_LAUNCH(GL)                                                                               \
-  do {                                                                                                 \
-    if (fast) hipLaunchKernelGGL((qk_rope_kernel<GL, APPEND, true>), grid, block, 0, s, a);            \
-    else hipLaunchKernelGGL((qk_rope_kernel<GL, APPEND, false>), grid, block, 0, s, a);                \
-  } while (0)
-  if (gl == 4) GQ_QK_LAUNCH(4);
-  else if (gl == 8) GQ_QK_LAUNCH(8);
-  else if (gl == 16) GQ_QK_LAUNCH(16);
-  else GQ_QK_LAUNCH(32);
-#undef GQ_QK_LAUNCH
+  if (a.hd <= 32) launch_qk_gl<4, APPEND>(a, heads, s);
+  else if (a.hd <= 64) launch_qk_gl<8, APPEND>(a, heads, s);
+  else if (a.hd <= 128) launch_qk_gl<16, APPEND>(a, heads, s);
+  else launch_qk_gl<32, APPEND>(a, heads, s);
   return hipGetLastError();
 }
 
@@ -349,6 +424,7 @@ hipError_t launch_qk_rope(const HeadArgs& h, int n_tok, int hd, const int32_t* p
   a.n_tok = n_tok;
   a.hd = hd;
   a.eps = eps;
+  a.inv_hd = 1.0 / hd;
   return launch_qk<false>(a, h.n_head, s);
 }
 
@@ -363,13 +439,19 @@ hipError_t launch_kv4_append(const Kv4Args& c, const HeadArgs& q, const HeadArgs
   a.n_tok = c.n_tok;
   a.hd = c.hd;
   a.eps = eps;
+  a.inv_hd = 1.0 / c.hd;
   return launch_qk<true>(a, q.n_head + k.n_head + v.n_head, s);
 }
 
 hipError_t launch_kv4_read(const Kv4Args& c, float* K, float* V, hipStream_t s) {
-  const int passes = (2 * c.n_kv * (c.hd / 8) + kThreads - 1) / kThreads;
-  const int gx = std::min(c.n_tok, 1 << 20), gy = c.n_tok >= 1024 ? 1 : std::min(passes, 65535);
-  hipLaunchKernelGGL(kv4_read_kernel, dim3(gx, gy), dim3(kThreads), 0, s, c, K, V);
+  if (c.n_tok >= kManyRows) {
+    constexpr int TOK = 16;
+    const int gx = std::min((c.n_tok + TOK - 1) / TOK, 1 << 20);
+    hipLaunchKernelGGL(kv4_read_kernel<TOK>, dim3(gx), dim3(kThreads), 0, s, c, K, V);
+  } else {
+    const int passes = (int)std::min<int64_t>(((int64_t)2 * c.n_kv * (c.hd / 4) + kThreads - 1) / kThreads, 4096);
+    hipLaunchKernelGGL(kv4_read_kernel<1>, dim3(c.n_tok, passes), dim3(kThreads), 0, s, c, K, V);
+  }
   return hipGetLastError();
 }
 

@@ -827,42 +827,57 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
   }
 }
 
-// The parts of a split row added up: a wave per row, the maxima and totals
-// first. Parts without keys have a maximum of minus infinity.
+// The parts of a split row added up: a workgroup per row, LANES = head_dim / 4
+// lanes (rounded up to a power of two) per part, so that 1024 / head_dim parts
+// are read at a time; then their sums in LDS, in a fixed order. Parts without
+// keys have a maximum of minus infinity and are skipped.
+template <int LANES>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
+  constexpr int GROUPS = kThreads / LANES;
+  __shared__ f32x4 so[GROUPS][LANES];
+  __shared__ float st[GROUPS], sm[kWaves];
   const Kv4Args& c = a.c;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t per = (int64_t)a.max_q * a.group, heads = (int64_t)c.n_seq * c.n_kv, rows = heads * per;
+  const int tid = threadIdx.x, sub = tid % LANES, g = tid / LANES;
+  const int64_t per = (int64_t)a.max_q * a.group, rows = (int64_t)c.n_seq * c.n_kv * per;
   const float* ml = a.part + rows * a.splits * c.hd;
-  for (int64_t i = (int64_t)blockIdx.x * kWaves + wave; i < rows; i += (int64_t)gridDim.x * kWaves) {
+  const bool on = sub * 4 < c.hd;
+  for (int64_t i = blockIdx.x; i < rows; i += gridDim.x) {
     const int64_t bh = i / per;
     const int r = (int)(i - bh * per), b = (int)(bh / c.n_kv), kvh = (int)(bh - (int64_t)b * c.n_kv);
     const SeqRows s = seq_rows(c, b);
     if (r / a.group >= s.n) continue;
     const int64_t slot0 = bh * a.splits * per + r;
     float M = -INFINITY;
-    for (int p = lane; p < a.splits; p += 64) M = fmaxf(M, ml[2 * (slot0 + p * per)]);
+    for (int p = tid; p < a.splits; p += kThreads) M = fmaxf(M, ml[2 * (slot0 + p * per)]);
 #pragma unroll
     for (int w = 32; w > 0; w /= 2) M = fmaxf(M, __shfl_xor(M, w));
+    if ((tid & 63) == 0) sm[tid >> 6] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm[w]);
     const float base = M == -INFINITY ? 0.f : M;
-    float tot = 0.f, sum[4] = {};
-    for (int p = 0; p < a.splits; ++p) {
-      const float pm = ml[2 * (slot0 + p * per)];
-      if (pm == -INFINITY && ml[2 * (slot0 + p * per) + 1] == 0.f) continue;
+    float tot = 0.f;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int p = g; p < a.splits; p += GROUPS) {
+      const float pm = ml[2 * (slot0 + p * per)], pl = ml[2 * (slot0 + p * per) + 1];
+      const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + (slot0 + p * per) * c.hd + (on ? sub * 4 : 0));
+      const bool none = pm == -INFINITY && pl == 0.f;
       const float f = __builtin_amdgcn_exp2f(pm - base);
-      tot += f * ml[2 * (slot0 + p * per) + 1];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int ch = lane + 64 * e;
-        if (ch < c.hd) sum[e] += f * a.part[(slot0 + p * per) * c.hd + ch];
-      }
+      if (!none) tot += f * pl, sum += f * v;
     }
-    float* out = a.out + (int64_t)(s.first + r / a.group) * a.out_stride + (int64_t)(kvh * a.group + r % a.group) * c.hd;
+    so[g][sub] = sum;
+    if (sub == 0) st[g] = tot;
+    __syncthreads();
+    if (g == 0 && on) {
+      float t = st[0];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int ch = lane + 64 * e;
-      if (ch < c.hd) out[ch] = tot == 0.f ? 0.f : sum[e] / tot;
+      for (int k = 1; k < GROUPS; ++k) t += st[k], sum += so[k][sub];
+      const f32x4 o = t == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : sum / t;
+      float* out = a.out + (int64_t)(s.first + r / a.group) * a.out_stride + (int64_t)(kvh * a.group + r % a.group) * c.hd;
+      __builtin_memcpy(__builtin_assume_aligned(out + sub * 4, 4), &o, 16);
     }
+    __syncthreads();
   }
 }
 
@@ -911,8 +926,10 @@ hipError_t launch_kv4_attn(const AttnArgs& a, hipStream_t s) {
   }
   if (a.splits > 1) {
     const int64_t all = a.c.n_seq * (int64_t)a.c.n_kv * rows;
-    const int64_t wgs = std::min<int64_t>((all + kWaves - 1) / kWaves, 1 << 20);
-    hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)wgs), dim3(kThreads), 0, s, a);
+    const dim3 wgs((unsigned)std::min<int64_t>(all, 1 << 20));
+    if (a.c.hd <= 64) hipLaunchKernelGGL(attn_join_kernel<16>, wgs, dim3(kThreads), 0, s, a);
+    else if (a.c.hd <= 128) hipLaunchKernelGGL(attn_join_kernel<32>, wgs, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL(attn_join_kernel<64>, wgs, dim3(kThreads), 0, s, a);
   }
   return hipGetLastError();
 }
