@@ -40,6 +40,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr float kSlack = 6.f;
+constexpr int kBufferFlags = 0x00020000;  // raw 32-bit data
 constexpr int kTile = 32;  // keys that a wave of the row kernel takes at once
 
 // The keys that a row at position pos sees: lo .. hi - 1 (none: hi <= lo).
@@ -88,6 +89,20 @@ __device__ __forceinline__ h8 key_operand(uint32_t w, h2 d, h2 off) {
                two_values<1>(hi, d, off));
 }
 __host__ __device__ constexpr int slot_channel(int j) { return (j >> 1) + 4 * (j & 1); }
+
+// Two weights as fp16 hi parts; the empty asm keeps the pair packed, so that the
+// lo parts below read its halves in place (one v_fma_mix each).
+__device__ __forceinline__ h2 hi_parts(float p0, float p1) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  uint32_t b = __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{p0, p1}), h2));
+  __asm__("" : "+v"(b));
+  return __builtin_bit_cast(h2, b);
+}
+
+// p - hi, rounded to fp16 once (part = -1), or p itself (part = 0).
+__device__ __forceinline__ h2 lo_parts(h2 hi, float p0, float p1, float part) {
+  return h2{(_Float16)__builtin_fmaf((float)hi.x, part, p0), (_Float16)__builtin_fmaf((float)hi.y, part, p1)};
+}
 
 // The largest of a value over the four lanes l, l ^ 16, l ^ 32, l ^ 48, in all
 // of them; and the sum.
@@ -148,7 +163,7 @@ struct RowTile {
 };
 
 template <int D, bool FUSED>
-__global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn_rows_kernel(AttnArgs a) {
   typedef RowTile<D> Tile;
   constexpr int KW = Tile::KW, VW = Tile::VW, NT = D / 16;  // NT: matrix tiles of channels
   constexpr int ROWS = FUSED ? 8 : 16;
@@ -170,8 +185,16 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a) {
   const int kblk = g * (KW * 8) / 32, vblk0 = m * NT / 32;
   const bool v_on = m * NT < hd;
   const int vcol = v_on ? m * (NT / 2) : 0, vblk = v_on ? vblk0 : 0;
+  // (byte offsets inside a head's part of a page; a lane without channels
+  // points past it, where buffer loads give 0: a scale of 0)
+  constexpr int kNowhere = 0x7FFFFF00;
   const int koff = m * row_b + kcol;
-  const int voff = 4 * g * row_b + vcol;
+  int voff[4], ksoff[Tile::KS];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) voff[j] = (4 * g + j) * row_b + vcol;
+#pragma unroll
+  for (int i = 0; i < Tile::KS; ++i) ksoff[i] = (kblk + i) * 32 < hd ? 2 * (((kblk + i) << lg) + m) : kNowhere;
+  const int vsoff = v_on ? 2 * ((vblk << lg) + 4 * g) : kNowhere;
   const int scale_at = kv4_code_bytes(hd, lg);
   const int64_t head_at = kv4_part(c, kvh, 0);
   const int part_b = kv4_part_bytes(hd, lg);
@@ -190,27 +213,95 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a) {
     const int lo = first.lo & ~(kTile - 1), hi = last.hi;
     const int tiles = hi > first.lo ? (hi - lo + kTile - 1) / kTile : 0;
     const int parts = a.splits * kWaves, mypart = split * kWaves + wave;
-    const int tile0 = (int)((int64_t)tiles * mypart / parts), tile1 = (int)((int64_t)tiles * (mypart + 1) / parts);
+    const int each = (int)((unsigned)tiles / (unsigned)parts), more = tiles - each * parts;
+    const int tile0 = mypart * each + (mypart < more ? mypart : more), tile1 = tile0 + each + (mypart < more ? 1 : 0);
+    const int begin = lo + tile0 * kTile, end = lo + tile1 * kTile;
 
     // the query operand: lane (m, g) holds the channels that its key lanes
-    // hold, of row m (FUSED: the hi part of row m, or the lo part of row m - 8)
+    // hold, of row m (FUSED: the hi part of row m, or the lo part of row m - 8);
+    // loaded first, and made operands with the first tile's loads in flight
+    const bool q_on = row < R;
+    const float* qr = a.q + (int64_t)(q_on ? t : s.first) * a.q_stride +
+                      (int64_t)(kvh * a.group + (q_on ? row % a.group : 0)) * hd;
+    f32x4 qx[KW][2];
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      const int c0 = (g * KW + w) * 8, at = c0 < hd ? c0 : 0;
+      qx[w][0] = load_f32x4(qr + at), qx[w][1] = load_f32x4(qr + at + 4);
+    }
+
+    const int32_t* table = c.table + (int64_t)b * c.table_stride;
+    const auto page_id = [&](int key) { return table[(key < hi ? key : hi - 1) >> lg]; };
+    // a page number that is none: nothing is read, and the scores are NaN
+    const auto page_ok = [&](int id) { return id >= 0 && id < c.n_pages; };
+    const auto page_buffer = [&](int id) {
+      const bool ok = page_ok(id);
+      return __builtin_amdgcn_make_buffer_rsrc(c.pages + (int64_t)(ok ? id : 0) * c.page_bytes + head_at, 0,
+                                               ok ? 2 * part_b : 0, kBufferFlags);
+    };
+    Tile x;
+    const auto load_keys = [&](int key0, int id0, int id1) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int id = u ? id1 : id0, slot0 = (key0 + 16 * u) & (P - 1);
+        const __amdgpu_buffer_rsrc_t rs = page_buffer(id);
+        if constexpr (KW == 2) {
+          const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, koff, slot0 * row_b, 0));
+          x.k[u][0] = v.x, x.k[u][1] = v.y;
+        } else {
+#pragma unroll
+          for (int w = 0; w < KW; w += 4) {
+            const u32x4 v =
+                __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, koff + 4 * w, slot0 * row_b, 0));
+            x.k[u][w] = v.x, x.k[u][w + 1] = v.y, x.k[u][w + 2] = v.z, x.k[u][w + 3] = v.w;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < Tile::KS; ++i)
+          x.ks[u][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, ksoff[i], scale_at + 2 * slot0, 0);
+      }
+    };
+    const auto load_values = [&](int key0, int id0, int id1) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int id = u ? id1 : id0, slot0 = (key0 + 16 * u) & (P - 1);
+        const __amdgpu_buffer_rsrc_t rs = page_buffer(id);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (D == 64) {
+            x.v[4 * u + j][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, voff[j], part_b + slot0 * row_b, 0);
+          } else if constexpr (D == 128) {
+            x.v[4 * u + j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, voff[j], part_b + slot0 * row_b, 0);
+          } else {
+            const u32x2 v = __builtin_bit_cast(
+                u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, voff[j], part_b + slot0 * row_b, 0));
+            x.v[4 * u + j][0] = v.x, x.v[4 * u + j][1] = v.y;
+          }
+        }
+        x.vs[u] = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, vsoff, part_b + scale_at + 2 * slot0, 0));
+      }
+    };
+
+    int id0 = 0, id1 = 0;
+    if (begin < end) {
+      id0 = page_id(begin), id1 = page_id(begin + 16);
+      load_keys(begin, id0, id1);
+      load_values(begin, id0, id1);
+    }
+
     h8 qh[KW], ql[FUSED ? 1 : KW];
     float down;
     {
-      const bool on = row < R;
-      const float* qr = a.q + (int64_t)(on ? t : s.first) * a.q_stride +
-                        (int64_t)(kvh * a.group + (on ? row % a.group : 0)) * hd;
-      float x[KW][8];
       float big = 0.f;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        const int c0 = (g * KW + w) * 8;
-        const bool in = on && c0 < hd;
-        const f32x4 u = load_f32x4(qr + (in ? c0 : 0)), v = load_f32x4(qr + (in ? c0 + 4 : 4));
+        const bool in = q_on && (g * KW + w) * 8 < hd;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[w][i] = in ? u[i] : 0.f, x[w][i + 4] = in ? v[i] : 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) big = fmaxf(big, __builtin_fabsf(x[w][i]));
+        for (int i = 0; i < 8; ++i) {
+          qx[w][i >> 2][i & 3] = in ? qx[w][i >> 2][i & 3] : 0.f;
+          big = fmaxf(big, __builtin_fabsf(qx[w][i >> 2][i & 3]));
+        }
       }
       const RowScale rs = row_scale(max_over_rows(big), a.scale);
       down = rs.down;
@@ -219,7 +310,8 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a) {
         h8 h, l;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float y = x[w][slot_channel(j)] * rs.up;
+          const int e = slot_channel(j);
+          const float y = qx[w][e >> 2][e & 3] * rs.up;
           h[j] = (_Float16)y;
           l[j] = (_Float16)(y - (float)h[j]);
         }
@@ -232,75 +324,43 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a) {
       }
     }
 
-    const int32_t* table = c.table + (int64_t)b * c.table_stride;
-    const auto page_id = [&](int key) { return table[(key < hi ? key : hi - 1) >> lg]; };
-    const auto load = [&](Tile& x, int key0, int id0, int id1) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int id = u ? id1 : id0;
-        const bool ok = id >= 0 && id < c.n_pages;
-        const int slot0 = (key0 + 16 * u) & (P - 1);
-        const uint8_t* kp = c.pages + (int64_t)(ok ? id : 0) * c.page_bytes + head_at;
-        const uint8_t* kc = kp + slot0 * row_b + koff;
-        if constexpr (KW == 2) {
-          u32x2 v;
-          __builtin_memcpy(&v, __builtin_assume_aligned(kc, 8), 8);
-          x.k[u][0] = v.x, x.k[u][1] = v.y;
-        } else {
-#pragma unroll
-          for (int w = 0; w < KW; w += 4) {
-            u32x4 v;
-            __builtin_memcpy(&v, __builtin_assume_aligned(kc + 4 * w, 16), 16);
-            x.k[u][w] = v.x, x.k[u][w + 1] = v.y, x.k[u][w + 2] = v.z, x.k[u][w + 3] = v.w;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < Tile::KS; ++i) {
-          const bool in = (kblk + i) * 32 < hd;
-          const uint32_t d = load_u16(kp + scale_at + 2 * (((in ? kblk + i : 0) << lg) + slot0 + m));
-          x.ks[u][i] = ok ? (in ? d : 0u) : 0x7E00u;  // no page: NaN scores
-        }
-        const uint8_t* vc = kp + part_b + slot0 * row_b + voff;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (D == 64) {
-            x.v[4 * u + j][0] = load_u16(vc + j * row_b);
-          } else if constexpr (D == 128) {
-            x.v[4 * u + j][0] = load_u32(vc + j * row_b);
-          } else {
-            u32x2 v;
-            __builtin_memcpy(&v, __builtin_assume_aligned(vc + j * row_b, 8), 8);
-            x.v[4 * u + j][0] = v.x, x.v[4 * u + j][1] = v.y;
-          }
-        }
-        u32x2 d;
-        __builtin_memcpy(&d, __builtin_assume_aligned(kp + part_b + scale_at + 2 * ((vblk << lg) + slot0 + 4 * g), 8), 8);
-        x.vs[u] = ok && v_on ? d : u32x2{0u, 0u};
-      }
-    };
-
     f32x4 o[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     float mx = -INFINITY, l = 0.f;
 
-    const auto compute = [&](Tile& x, int key0) {
+    // Keys and values have one set of registers each: the next tile's keys are
+    // requested when this tile's have been multiplied, its values likewise, and
+    // page numbers a tile before that. The loads past the last tile repeat it:
+    // were they skipped, the waits would have to be for all loads in flight.
+    // (The scheduling barriers keep the parts of a tile apart, whose operands
+    // would otherwise be live at once.)
+    for (int key0 = begin; key0 < end; key0 += kTile) {
+      const int next = key0 + kTile < end ? key0 + kTile : key0;
+      const int jd0 = page_id(next), jd1 = page_id(next + 16);
       // scores: rows are this half tile's keys 4 g + r, columns query rows
       f32x4 sc[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+        __builtin_amdgcn_sched_barrier(0);
         sc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const uint32_t none = page_ok(u ? id1 : id0) ? 0u : 0x7E00u;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-          const h2 d = both(x.ks[u][w / 4]);
+          const h2 d = both(x.ks[u][w / 4] | none);
           const h8 k = key_operand(x.k[u][w], d, minus8(d));
           sc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[w], sc[u], 0, 0, 0);
           if constexpr (!FUSED) sc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[w], sc[u], 0, 0, 0);
         }
-        if constexpr (FUSED) {
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      load_keys(next, jd0, jd1);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (FUSED) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int r = 0; r < 4; ++r) sc[u][r] += dpp_f32<0x128>(sc[u][r]);  // row_ror:8: hi + lo
-        }
       }
       // masks, in tiles that reach past some row's keys. There a value whose
       // scale is not finite must not meet the zero weight of a row that does
@@ -351,13 +411,12 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a) {
           const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][r], down, -base));
           const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][r + 1], down, -base));
           l += p0 + p1;
-          const h2 h = {(_Float16)p0, (_Float16)p1};
-          // the lo part (FUSED: p itself in the hi columns)
-          const float r0 = __builtin_fmaf((float)h.x, part, p0), r1 = __builtin_fmaf((float)h.y, part, p1);
-          ph[2 * u + r / 2] = h;
-          pl[2 * u + r / 2] = h2{(_Float16)r0, (_Float16)r1};
+          // (FUSED: p itself in the hi columns)
+          ph[2 * u + r / 2] = hi_parts(p0, p1);
+          pl[2 * u + r / 2] = lo_parts(ph[2 * u + r / 2], p0, p1, part);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
       const h8 wl = as_h8(pl[0], pl[1], pl[2], pl[3]);
       const h8 wh = as_h8(ph[0], ph[1], ph[2], ph[3]);
       // values: pairs of keys side by side, channel by channel
@@ -371,6 +430,7 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a) {
       for (int w = 0; w < VW; ++w) {
 #pragma unroll
         for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
+          __builtin_amdgcn_sched_barrier(0);
           // bytes (2 half) and (2 half + 1) of the pairs' dwords, interleaved
           uint32_t lo4[4], hi4[4];
 #pragma unroll
@@ -396,24 +456,9 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a) {
                         two_values<1>(hi4[2], vd[2], voffs[2]), two_values<1>(hi4[3], vd[3], voffs[3])));
         }
       }
-    };
-
-    if (tile0 < tile1) {
-      Tile x0, x1;
-      int key = lo + tile0 * kTile;
-      const int end = lo + tile1 * kTile;
-      load(x0, key, page_id(key), page_id(key + 16));
-      // page numbers run two tiles ahead of the compute, data one
-      int id0 = page_id(key + kTile), id1 = page_id(key + kTile + 16);
-      for (; key < end; key += 2 * kTile) {
-        int jd0 = page_id(key + 2 * kTile), jd1 = page_id(key + 2 * kTile + 16);
-        if (key + kTile < end) load(x1, key + kTile, id0, id1);
-        compute(x0, key);
-        if (key + kTile >= end) break;
-        id0 = page_id(key + 3 * kTile), id1 = page_id(key + 3 * kTile + 16);
-        if (key + 2 * kTile < end) load(x0, key + 2 * kTile, jd0, jd1);
-        compute(x1, key + kTile);
-      }
+      __builtin_amdgcn_sched_barrier(0);
+      id0 = jd0, id1 = jd1;
+      load_values(next, id0, id1);
     }
     l = sum_over_rows(l);
 
@@ -477,51 +522,37 @@ __global__ __launch_bounds__(kThreads) void attn_rows_kernel(AttnArgs a) {
 // Many rows a sequence (prompts and their chunks). A workgroup owns 128 rows
 // of one kv head -- consecutive tokens times the query heads that share it, 32
 // rows a wave -- and walks the keys 64 at a time (32 for heads past 128
-// channels). The tile is dequantised once into LDS as fp16 by all four waves
-// (waves 0, 1 the keys, 2, 3 the values), two tiles deep: the next tile's
-// codes are in flight while this one is computed, and one barrier a tile is
-// enough.
-//   LDS: keys [key][channel], values [channel][key], in 16-byte chunks whose
-//   place in the row is xored with the row, so that the 16 lanes that read
-//   (or write) one chunk column at a time cover all 64 banks.
+// channels). The tile is dequantised once into LDS as fp16, two tiles deep:
+// each wave brings in 16 keys of up to 128 channels (one page, so its loads
+// take the page from scalar registers); the next tile's codes are in flight
+// while this one is computed, and one barrier a tile is enough.
+//   LDS: keys [key][channel], values [channel][key], rows padded by 16 bytes:
+//   the 16 lanes that read (or write) one chunk column at a time cover all 64
+//   banks, and every address is one register and an immediate.
 //   S^T (32 keys x 32 rows per matrix instruction) leaves a row's scores in
 //   the lanes l and l ^ 32; the weights go straight into the second product,
-//   whose keys are ordered as the scores lie (chunk 2 t + h of a value row
-//   holds keys 16 t + 4 h + 0 .. 3 and 16 t + 8 + 4 h + 0 .. 3).
+//   whose keys are ordered as the scores lie: chunk 2 t + h of a value row
+//   holds keys 16 t + 4 h + 0 .. 3 and 16 t + 8 + 4 h + 0 .. 3.
 // Bound: issue. Per wave and 64 keys of 128 channels, 128 matrix instructions
 // (about 37 cycles each, which do not overlap vector instructions on this
-// GPU) and about 600 vector ones for softmax and dequantisation.
+// GPU) and about 400 vector ones for softmax and dequantisation.
 template <int D>
 struct TileCfg {
-  static constexpr int KT = D > 128 ? 32 : 64;        // keys per tile
-  static constexpr int KPT = KT * D / 32 / 128;       // key blocks staged per thread (waves 0, 1)
-  static constexpr int VTASKS = KT / 8 * (D / 8);     // value tasks (waves 2, 3): 8 keys x 8 channels
-  static constexpr int CH = D / 8;                    // chunks of a key row
-  static constexpr int VCH = KT / 8;                  // chunks of a value row
-  static_assert(VTASKS <= 128, "one value task per thread");
+  static constexpr int KT = D > 128 ? 32 : 64;      // keys per tile
+  static constexpr int DC = D > 128 ? 128 : D;      // channels that a wave brings in
+  static constexpr int KROW = 2 * D + 16;           // bytes of a key row
+  static constexpr int VROW = 2 * KT + 16;          // bytes of a value row (one channel)
+  static constexpr int KBYTES = KT * KROW, VBYTES = D * VROW;
 };
-
-template <int D>
-__device__ __forceinline__ int key_chunk(int key, int c) {
-  const int x = D == 64 ? (key >> 1) & 7 : key & 15;
-  return key * (D / 8) + (c ^ x);
-}
-
-template <int D>
-__device__ __forceinline__ int value_chunk(int row, int c) {
-  constexpr int VCH = TileCfg<D>::VCH;
-  const int x = VCH == 8 ? (row >> 1) & 7 : (row >> 2) & 3;
-  return row * VCH + (c ^ x);
-}
 
 constexpr int kTileRows = 128;
 
 template <int D>
 __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(AttnArgs a) {
   typedef TileCfg<D> C;
-  constexpr int KT = C::KT, KB = KT / 32, NT = D / 32, KS = D / 16;
-  __shared__ h8 kbuf[2][KT * D / 8];
-  __shared__ h8 vbuf[2][KT * D / 8];
+  constexpr int KT = C::KT, KB = KT / 32, NT = D / 32, KS = D / 16, DC = C::DC;
+  constexpr int KW = DC / 32;  // dwords of a key that a lane brings in
+  __shared__ __align__(16) uint8_t lds[2][C::KBYTES + C::VBYTES];
   __shared__ unsigned long long bad[3];  // keys of a masked tile whose value has a scale that is not finite
 
   const Kv4Args& c = a.c;
@@ -536,6 +567,27 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
   const int scale_at = kv4_code_bytes(hd, lg), part_b = kv4_part_bytes(hd, lg);
   const int64_t head_at = kv4_part(c, kvh, 0);
 
+  // Staging: this wave's 16 keys of the tile, channels from sub_c on. Keys:
+  // lane (key lane >> 2, quarter lane & 3) reads DC / 4 channels, one scale.
+  // Values: lane (m16, kg) reads DC / 16 channels of keys 4 kg .. 4 kg + 3;
+  // the groups are dealt so that a half wave's 8-byte writes meet no bank twice.
+  const int sub_key = (wave * DC / D) * 16, sub_c = (wave * DC) % D;
+  constexpr int kNowhere = 0x7FFFFF00;
+  const int skey = lane >> 2, squart = lane & 3;
+  const int sk_c = sub_c + squart * (DC / 4);
+  const int koff = skey * row_b + (sk_c < hd ? sk_c / 2 : 0);
+  const int ksoff = sk_c < hd ? 2 * (((sk_c / 32) << lg) + skey) : kNowhere;
+  const int m16 = lane & 15, kg = ((lane >> 4) & 1) * 2 + (lane >> 5);
+  const int sv_c = sub_c + m16 * (DC / 16);
+  const int voff = 4 * kg * row_b + (sv_c < hd ? sv_c / 2 : 0);
+  const int vsoff = sv_c < hd ? 2 * (((sv_c / 32) << lg) + 4 * kg) : kNowhere;
+  const int kwrite = (sub_key + skey) * C::KROW + sk_c * 2;
+  // value rows: channel i of dword w is row i (D / 8) + w; a dword's even
+  // channels come first (D = 64: a lane has every second channel of a dword)
+  const int vrow = D == 64 ? (m16 & 1) * 8 + (m16 >> 1) : sub_c / 8 + m16;
+  const int vwrite = C::KBYTES + vrow * C::VROW + 2 * sub_key + 16 * (kg & 1) + 8 * (kg >> 1);
+  const int kread = m * C::KROW + 16 * h, vread = C::KBYTES + m * C::VROW + 16 * h;
+
   for (int b = blockIdx.y; b < c.n_seq; b += gridDim.y) {
     const SeqRows s = seq_rows(c, b);
     const int n = s.n < a.max_q ? s.n : a.max_q;
@@ -546,7 +598,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
     const Seen first = seen_keys(a, pos0 + row0 / a.group, len), last = seen_keys(a, pos0 + rlast / a.group, len);
     const int lo = first.lo & ~(KT - 1), hi = last.hi;
     const int tiles = hi > first.lo ? (hi - lo + KT - 1) / KT : 0;
-    const int tile0 = (int)((int64_t)tiles * split / a.splits), tile1 = (int)((int64_t)tiles * (split + 1) / a.splits);
+    const int each = (int)((unsigned)tiles / (unsigned)a.splits), more = tiles - each * a.splits;
+    const int tile0 = split * each + (split < more ? split : more), tile1 = tile0 + each + (split < more ? 1 : 0);
     const int32_t* table = c.table + (int64_t)b * c.table_stride;
 
     const int row = row0 + wave * 32 + m;
@@ -555,105 +608,78 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
     const int head = kvh * a.group + (row_on ? row - tok * a.group : 0);
     const Seen mine = seen_keys(a, pos0 + tok, len);
 
-    // staging: what this thread brings in of each tile
-    const bool key_side = wave < 2;
-    const int st = tid & 127;
-    const bool value_on = !key_side && st < C::VTASKS;
-    const int vcol = st % (D / 8), vchunk = st / (D / 8);
-    const int vkey = 16 * (vchunk >> 1) + 4 * (vchunk & 1);  // and 8 further on
-    const bool vin = vcol * 8 < hd;
-    u32x4 raw[C::KPT > 2 ? C::KPT : 2];
-    uint32_t rawd[4];
-    int ids[C::KPT];
+    uint32_t raw_k[KW], raw_v[4];
+    uint32_t raw_ks;
+    u32x2 raw_vs;
+    int id = 0;  // the page of the wave's keys in the tile that is fetched next
 
-    const auto find = [&](int tile) {  // page numbers of a tile's tasks
-#pragma unroll
-      for (int i = 0; i < C::KPT; ++i) {
-        const int key = lo + tile * KT + (key_side ? (st + 128 * i) / (D / 32) : vkey);
-        if (key_side || i == 0) ids[i] = table[(key < hi ? key : hi - 1) >> lg];
-      }
+    const auto find = [&](int tile) {
+      const int key = lo + tile * KT + sub_key;
+      id = table[(key < hi ? key : hi - 1) >> lg];
     };
     const auto fetch = [&](int tile) {
-      if (key_side) {
+      const int slot0 = (lo + tile * KT + sub_key) & (P - 1);
+      const bool ok = id >= 0 && id < c.n_pages;  // else nothing is read, and the scores are NaN
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          c.pages + (int64_t)(ok ? id : 0) * c.page_bytes + head_at, 0, ok ? 2 * part_b : 0, kBufferFlags);
+      const int code_at = slot0 * row_b, scales = scale_at + 2 * slot0;
+      if constexpr (KW == 2) {
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, koff, code_at, 0));
+        raw_k[0] = v.x, raw_k[1] = v.y;
+      } else {
+        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, koff, code_at, 0));
 #pragma unroll
-        for (int i = 0; i < C::KPT; ++i) {
-          const int id = st + 128 * i, blk = id % (D / 32), slot = (lo + tile * KT + id / (D / 32)) & (P - 1);
-          const bool ok = ids[i] >= 0 && ids[i] < c.n_pages, in = blk * 32 < hd;
-          const uint8_t* kp = c.pages + (int64_t)(ok ? ids[i] : 0) * c.page_bytes + head_at;
-          __builtin_memcpy(&raw[i], __builtin_assume_aligned(kp + slot * row_b + (in ? blk : 0) * 16, 16), 16);
-          const uint32_t d = load_u16(kp + scale_at + 2 * (((in ? blk : 0) << lg) + slot));
-          rawd[i] = ok ? (in ? d : 0u) : 0x7E00u;
-        }
-      } else if (value_on) {
-        const int slot = (lo + tile * KT + vkey) & (P - 1);
-        const bool ok = ids[0] >= 0 && ids[0] < c.n_pages;
-        const uint8_t* vp = c.pages + (int64_t)(ok ? ids[0] : 0) * c.page_bytes + head_at + part_b;
-        const uint8_t* vc = vp + slot * row_b + (vin ? vcol : 0) * 4;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          raw[0][j] = load_u32(vc + j * row_b);
-          raw[1][j] = load_u32(vc + (8 + j) * row_b);
-        }
-        const uint8_t* vs = vp + scale_at + 2 * (((vin ? vcol / 4 : 0) << lg) + slot);
-        u32x2 d0, d1;
-        __builtin_memcpy(&d0, __builtin_assume_aligned(vs, 8), 8);
-        __builtin_memcpy(&d1, __builtin_assume_aligned(vs + 16, 8), 8);
-        const bool on = ok && vin;
-        rawd[0] = on ? d0.x : 0u, rawd[1] = on ? d0.y : 0u, rawd[2] = on ? d1.x : 0u, rawd[3] = on ? d1.y : 0u;
+        for (int w = 0; w < 4; ++w) raw_k[w] = v[w];
       }
+      raw_ks = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, ksoff, scales, 0) | (ok ? 0u : 0x7E00u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (D == 64)
+          raw_v[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, voff, part_b + code_at + j * row_b, 0);
+        else
+          raw_v[j] = __builtin_amdgcn_raw_buffer_load_b32(rs, voff, part_b + code_at + j * row_b, 0);
+      }
+      raw_vs = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, vsoff, part_b + scales, 0));
     };
     const auto masked = [&](int tile) {
       const int key0 = lo + tile * KT;
       return key0 + KT > first.hi || key0 < last.lo;
     };
     const auto stage = [&](int tile) {
-      const int buf = tile & 1;
-      if (tid == 0 && masked(tile + 1)) bad[(tile + 1) % 3] = 0;
-      if (key_side) {
+      uint8_t* buf = lds[tile & 1];
+      if (masked(tile + 1) && tid == 0) bad[(tile + 1) % 3] = 0;
+      {
+        const h2 d = both(raw_ks), off = minus8(d);
 #pragma unroll
-        for (int i = 0; i < C::KPT; ++i) {
-          const int id = st + 128 * i, blk = id % (D / 32), key = id / (D / 32);
-          const h2 d = both(rawd[i]), off = minus8(d);
+        for (int w = 0; w < KW; ++w)
+          *reinterpret_cast<h8*>(buf + kwrite + 16 * w) = key_operand(raw_k[w], d, off);
+      }
+      if (masked(tile)) {
+        const int key0 = lo + tile * KT + sub_key + 4 * kg;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) kbuf[buf][key_chunk<D>(key, blk * 4 + w)] = key_operand(raw[i][w], d, off);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t bits = (raw_vs[j >> 1] >> (16 * (j & 1))) & 0xFFFF;
+          const bool out = key0 + j >= hi, inf = (bits & 0x7C00) == 0x7C00;
+          if (inf && !out) atomicOr(&bad[tile % 3], 1ull << (sub_key + 4 * kg + j));
+          if (inf || out) raw_vs[j >> 1] &= j & 1 ? 0x0000FFFFu : 0xFFFF0000u;
         }
-      } else if (value_on) {
-        if (masked(tile)) {
-          const int key0 = lo + tile * KT + vkey;
+      }
+      const h2 d0 = __builtin_bit_cast(h2, (uint32_t)raw_vs.x), d1 = __builtin_bit_cast(h2, (uint32_t)raw_vs.y);
+      const h2 off0 = minus8(d0), off1 = minus8(d1);
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const int k = (p < 4 ? 0 : 4) + p;  // 0 .. 3, 8 .. 11
-            const uint32_t bits = (rawd[p >> 1] >> (16 * (p & 1))) & 0xFFFF;
-            const bool out = key0 + k >= hi, inf = (bits & 0x7C00) == 0x7C00;
-            if (inf && !out) atomicOr(&bad[tile % 3], 1ull << (vkey + k));
-            if (inf || out) rawd[p >> 1] &= p & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-          }
-        }
-        h2 d[4], off[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) d[p] = __builtin_bit_cast(h2, rawd[p]), off[p] = minus8(d[p]);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t lo4[4], hi4[4];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint32_t y = __builtin_amdgcn_perm(raw[p >> 1][2 * (p & 1) + 1], raw[p >> 1][2 * (p & 1)],
-                                                     half ? 0x07030602u : 0x05010400u);
-            lo4[p] = y & 0x0F0F0F0Fu;
-            hi4[p] = (y >> 4) & 0x0F0F0F0Fu;
-          }
-          const auto put = [&](int i, h8 v) {  // channel 2 i + half of the dword
-            vbuf[buf][value_chunk<D>((2 * i + half) * (D / 8) + vcol, vchunk)] = v;
-          };
-          put(0, as_h8(two_values<0>(lo4[0], d[0], off[0]), two_values<0>(lo4[1], d[1], off[1]),
-                       two_values<0>(lo4[2], d[2], off[2]), two_values<0>(lo4[3], d[3], off[3])));
-          put(1, as_h8(two_values<0>(hi4[0], d[0], off[0]), two_values<0>(hi4[1], d[1], off[1]),
-                       two_values<0>(hi4[2], d[2], off[2]), two_values<0>(hi4[3], d[3], off[3])));
-          put(2, as_h8(two_values<1>(lo4[0], d[0], off[0]), two_values<1>(lo4[1], d[1], off[1]),
-                       two_values<1>(lo4[2], d[2], off[2]), two_values<1>(lo4[3], d[3], off[3])));
-          put(3, as_h8(two_values<1>(hi4[0], d[0], off[0]), two_values<1>(hi4[1], d[1], off[1]),
-                       two_values<1>(hi4[2], d[2], off[2]), two_values<1>(hi4[3], d[3], off[3])));
-        }
+      for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
+        const uint32_t sel = half ? 0x07030602u : 0x05010400u;
+        const uint32_t y0 = __builtin_amdgcn_perm(raw_v[1], raw_v[0], sel), y1 = __builtin_amdgcn_perm(raw_v[3], raw_v[2], sel);
+        const uint32_t lo0 = y0 & 0x0F0F0F0Fu, lo1 = y1 & 0x0F0F0F0Fu;
+        const uint32_t hi0 = (y0 >> 4) & 0x0F0F0F0Fu, hi1 = (y1 >> 4) & 0x0F0F0F0Fu;
+        const auto put = [&](int i, h2 u, h2 v) {  // channel 2 i + half of the dword (D = 64: 2 i + m16 & 1)
+          u32x2 x = {__builtin_bit_cast(uint32_t, u), __builtin_bit_cast(uint32_t, v)};
+          *reinterpret_cast<u32x2*>(buf + vwrite + (2 * i + half) * (D / 8) * C::VROW) = x;
+        };
+        put(0, two_values<0>(lo0, d0, off0), two_values<0>(lo1, d1, off1));
+        put(1, two_values<0>(hi0, d0, off0), two_values<0>(hi1, d1, off1));
+        put(2, two_values<1>(lo0, d0, off0), two_values<1>(lo1, d1, off1));
+        put(3, two_values<1>(hi0, d0, off0), two_values<1>(hi1, d1, off1));
       }
     };
 
@@ -661,7 +687,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
     if (tile0 < tile1) {
       find(tile0);
       fetch(tile0);
-      if (tile0 + 1 < tile1) find(tile0 + 1);
+      find(tile0 + 1);
     }
 
     // the query operand, hi and lo parts
@@ -702,90 +728,91 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
       for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
     float mx = -INFINITY, l = 0.f;
 
+    float minus1 = -1.f;  // kept from being folded, so that p - hi and its rounding are one v_fma_mix
+    __asm__("" : "+s"(minus1));
     __syncthreads();  // bad is clear
     if (tile0 < tile1) {
       stage(tile0);
-      if (tile0 + 1 < tile1) fetch(tile0 + 1);
-      if (tile0 + 2 < tile1) find(tile0 + 2);
+      fetch(tile0 + 1);  // (past the last tile, its page again)
+      find(tile0 + 2);
     }
     __syncthreads();
     for (int tile = tile0; tile < tile1; ++tile) {
-      const int buf = tile & 1, key0 = lo + tile * KT;
-      f32x16 sc[KB];
+      const uint8_t* buf = lds[tile & 1];
+      const int key0 = lo + tile * KT;
+      // 32 keys at a time, which keeps the scores and weights in 32 registers
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
+        f32x16 sc;
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) sc[k][r] = 0.f;
+        for (int r = 0; r < 16; ++r) sc[r] = 0.f;
 #pragma unroll
         for (int w = 0; w < KS; ++w) {
-          const h8 x = kbuf[buf][key_chunk<D>(32 * k + m, 2 * w + h)];
-          sc[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, qh[w], sc[k], 0, 0, 0);
-          sc[k] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, ql[w], sc[k], 0, 0, 0);
+          const h8 x = *reinterpret_cast<const h8*>(buf + kread + 32 * k * C::KROW + 32 * w);
+          sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, qh[w], sc, 0, 0, 0);
+          sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, ql[w], sc, 0, 0, 0);
         }
-      }
-      if (masked(tile)) {
-        const unsigned long long bm = bad[tile % 3];
-#pragma unroll
-        for (int k = 0; k < KB; ++k) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (masked(tile)) {
+          const unsigned long long bm = bad[tile % 3];
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int at = 32 * k + 8 * (r >> 2) + 4 * h + (r & 3), key = key0 + at;
-            if (bm >> at & 1) sc[k][r] = __builtin_nanf("");
-            if (key < mine.lo || key >= mine.hi) sc[k][r] = -INFINITY;
+            if (bm >> at & 1) sc[r] = __builtin_nanf("");
+            if (key < mine.lo || key >= mine.hi) sc[r] = -INFINITY;
           }
         }
-      }
-      float top = sc[0][0];
+        float top = sc[0];
 #pragma unroll
-      for (int k = 0; k < KB; ++k)
+        for (int r = 1; r < 16; ++r) top = fmaxf(top, sc[r]);
+        {
+          const uint32_t u = __builtin_bit_cast(uint32_t, top);
+          const auto both_halves = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+          top = fmaxf(__builtin_bit_cast(float, (uint32_t)both_halves[0]),
+                      __builtin_bit_cast(float, (uint32_t)both_halves[1])) * down;
+        }
+        if (__any(top > mx + kSlack)) {
+          const float nm = fmaxf(mx, top);
+          const float f = __builtin_amdgcn_exp2f(mx - (nm == -INFINITY ? 0.f : nm));
+          mx = nm;
+          l *= f;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[k][r]);
-      {
-        const uint32_t u = __builtin_bit_cast(uint32_t, top);
-        const auto both_halves = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-        top = fmaxf(__builtin_bit_cast(float, (uint32_t)both_halves[0]),
-                    __builtin_bit_cast(float, (uint32_t)both_halves[1])) * down;
-      }
-      if (__any(top > mx + kSlack)) {
-        const float nm = fmaxf(mx, top);
-        const float f = __builtin_amdgcn_exp2f(mx - (nm == -INFINITY ? 0.f : nm));
-        mx = nm;
-        l *= f;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) o[i] *= f;
-      }
-      const float base = mx == -INFINITY ? 0.f : mx;
-      h8 ph[2 * KB], pl[2 * KB];
-#pragma unroll
-      for (int k = 0; k < KB; ++k) {
+          for (int i = 0; i < NT; ++i) o[i] *= f;
+        }
+        const float base = mx == -INFINITY ? 0.f : mx;
+        h8 ph[2], pl[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           h2 hs[4], ls[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[k][8 * t + 2 * r], down, -base));
-            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[k][8 * t + 2 * r + 1], down, -base));
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * t + 2 * r], down, -base));
+            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * t + 2 * r + 1], down, -base));
             l += p0 + p1;
-            hs[r] = h2{(_Float16)p0, (_Float16)p1};
-            ls[r] = h2{(_Float16)(p0 - (float)hs[r].x), (_Float16)(p1 - (float)hs[r].y)};
+            hs[r] = hi_parts(p0, p1);
+            ls[r] = lo_parts(hs[r], p0, p1, minus1);
           }
-          ph[2 * k + t] = as_h8(hs[0], hs[1], hs[2], hs[3]);
-          pl[2 * k + t] = as_h8(ls[0], ls[1], ls[2], ls[3]);
+          ph[t] = as_h8(hs[0], hs[1], hs[2], hs[3]);
+          pl[t] = as_h8(ls[0], ls[1], ls[2], ls[3]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const h8 x = *reinterpret_cast<const h8*>(buf + vread + 32 * i * C::VROW + 32 * (2 * k + t));
+            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, ph[t], o[i], 0, 0, 0);
+            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, pl[t], o[i], 0, 0, 0);
+          }
         }
       }
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-#pragma unroll
-        for (int t = 0; t < 2 * KB; ++t) {
-          const h8 x = vbuf[buf][value_chunk<D>(32 * i + m, 2 * t + h)];
-          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, ph[t], o[i], 0, 0, 0);
-          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, pl[t], o[i], 0, 0, 0);
-        }
-      }
+      __builtin_amdgcn_sched_barrier(0);
       if (tile + 1 < tile1) {
         stage(tile + 1);
-        if (tile + 2 < tile1) fetch(tile + 2);
-        if (tile + 3 < tile1) find(tile + 3);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(tile + 2);
+        find(tile + 3);
       }
       __syncthreads();
     }
@@ -902,14 +929,24 @@ void launch_tiles(const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Parts that a sequence's keys are cut into: enough workgroups to fill the
-// GPU (four per CU for the row kernel, two for the tile kernel), none with
-// less than 256 keys.
+// Parts that a sequence's keys are cut into. A part costs its workgroup about
+// 6 us of start and finish and the join its sums, so parts are made only
+//   - to fill the GPU: up to 512 workgroups, of at least 512 keys each for the
+//     row kernel (one sequence of 333 keys: 13.5 us whole, 18.5 in two) and
+//     256 for the tile kernel, whose workgroups are that much slower (64
+//     positions over 2048 keys: 31 us with 256, 38 with 512); more does not
+//     pay (65536 keys, 8 kv heads: 26.5 us with 512, 32.4 with 1024);
+//   - for the row kernel, to even out sequences of different lengths: up to
+//     2048 workgroups of at least 1024 keys (32 sequences of 8k to 16k keys:
+//     99.7 us with 2048, 105 with 1024, 117 with 512; 4 sequences: 22.6 us
+//     with 1024 keys each, 25.3 with 512).
 int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len) {
   if (n_seq <= 0 || rows <= 0) return 1;
-  const int64_t tiles = rows <= kRowKernelRows ? 1 : (rows + kTileRows - 1) / kTileRows;
-  const int64_t want = (rows <= kRowKernelRows ? 1024 : 512) / std::max<int64_t>(1, n_seq * n_kv * tiles);
-  return (int)std::max<int64_t>(1, std::min(want, (max_len + 255) / 256));
+  const bool few = rows <= kRowKernelRows;
+  const int64_t base = n_seq * n_kv * (few ? 1 : (rows + kTileRows - 1) / kTileRows);
+  const int64_t fill = std::min((max_len + (few ? 511 : 255)) / (few ? 512 : 256), 512 / base);
+  const int64_t even = few ? std::min((max_len + 1023) / 1024, 2048 / base) : 1;
+  return (int)std::max<int64_t>({1, fill, even});
 }
 
 hipError_t launch_kv4_attn(const AttnArgs& a, hipStream_t s) {

@@ -280,6 +280,22 @@ def test_read_descending_offsets_and_whole_sequences(gq):
     assert np.array_equal(only[40:43], b.sequence(1)[0])
 
 
+@pytest.mark.parametrize("n", [[40, 3], [1500, 2]])
+def test_read_into_unaligned_outputs(gq, n):
+    # four-byte aligned outputs, and only their rows are written
+    import torch
+    b = Batch(13, n, n, 64, 1, 64)
+    lens, q_start = b.dev()
+    size = b.n_tok * 64
+    bufs = [torch.full((size + 2,), 9.0, device="cuda") for _ in range(2)]
+    gq.gq_kv4_read(b.cache(gq), lens, b.n_tok, q_start, K=bufs[0][1:-1].view(-1, 1, 64), V=bufs[1][1:-1].view(-1, 1, 64))
+    kv = [b.sequence(s) for s in range(2)]
+    for i in range(2):
+        got = to_host(bufs[i])
+        assert got[0] == 9.0 and got[-1] == 9.0
+        assert np.array_equal(got[1:-1].reshape(-1, 1, 64), np.concatenate((kv[0][i], kv[1][i])))
+
+
 def test_append_captured(gq):
     """One decode step's append captured once and replayed with new tokens and
     lengths, eager work between; every replay's bytes against the oracle."""
