@@ -24,6 +24,7 @@
 // places where the second product takes its weights, so the softmax needs no
 // data movement but the maximum over the lanes that share a row.
 #include <algorithm>
+#include <type_traits>
 
 #include "gq_device.h"
 #include "kv4.h"
@@ -156,9 +157,12 @@ struct RowTile {
   static constexpr int KW = D / 32;             // dwords of a key per lane
   static constexpr int KS = KW > 4 ? KW / 4 : 1;  // scales of a key per lane
   static constexpr int VW = D >= 256 ? 2 : 1;   // dwords (D = 64: halves of one) of a value per lane
+  // (16-bit loads are kept as such until they are used: widening one where it
+  // is loaded would wait for it there)
+  typedef typename std::conditional<D == 64, uint16_t, uint32_t>::type Codes;
   uint32_t k[2][KW];
-  uint32_t ks[2][KS];
-  uint32_t v[8][VW];
+  uint16_t ks[2][KS];
+  Codes v[8][VW];
   u32x2 vs[2];
 };
 
@@ -258,7 +262,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn
         }
 #pragma unroll
         for (int i = 0; i < Tile::KS; ++i)
-          x.ks[u][i] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, ksoff[i], scale_at + 2 * slot0, 0);
+          x.ks[u][i] = __builtin_amdgcn_raw_buffer_load_b16(rs, ksoff[i], scale_at + 2 * slot0, 0);
       }
     };
     const auto load_values = [&](int key0, int id0, int id1) {
@@ -269,7 +273,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if constexpr (D == 64) {
-            x.v[4 * u + j][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, voff[j], part_b + slot0 * row_b, 0);
+            x.v[4 * u + j][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, voff[j], part_b + slot0 * row_b, 0);
           } else if constexpr (D == 128) {
             x.v[4 * u + j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, voff[j], part_b + slot0 * row_b, 0);
           } else {
@@ -608,16 +612,22 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
     const int head = kvh * a.group + (row_on ? row - tok * a.group : 0);
     const Seen mine = seen_keys(a, pos0 + tok, len);
 
-    uint32_t raw_k[KW], raw_v[4];
-    uint32_t raw_ks;
+    typename RowTile<D>::Codes raw_v[4];
+    uint32_t raw_k[KW], none = 0;
+    uint16_t raw_ks;
     u32x2 raw_vs;
-    int id = 0;  // the page of the wave's keys in the tile that is fetched next
-
+    // The page of the wave's keys in the tile that is fetched next. It is the
+    // same in all lanes, but is kept in a vector register until then (the zero
+    // that the compiler cannot see through): a scalar one would be waited for
+    // where it is loaded, and with it all loads in flight.
+    int zero, id_v = 0;
+    __asm__("v_mov_b32 %0, 0" : "=v"(zero));
     const auto find = [&](int tile) {
       const int key = lo + tile * KT + sub_key;
-      id = table[(key < hi ? key : hi - 1) >> lg];
+      id_v = table[((key < hi ? key : hi - 1) >> lg) + zero];
     };
     const auto fetch = [&](int tile) {
+      const int id = __builtin_amdgcn_readfirstlane(id_v);
       const int slot0 = (lo + tile * KT + sub_key) & (P - 1);
       const bool ok = id >= 0 && id < c.n_pages;  // else nothing is read, and the scores are NaN
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
@@ -631,11 +641,12 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
 #pragma unroll
         for (int w = 0; w < 4; ++w) raw_k[w] = v[w];
       }
-      raw_ks = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, ksoff, scales, 0) | (ok ? 0u : 0x7E00u);
+      raw_ks = __builtin_amdgcn_raw_buffer_load_b16(rs, ksoff, scales, 0);
+      none = ok ? 0u : 0x7E00u;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if constexpr (D == 64)
-          raw_v[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, voff, part_b + code_at + j * row_b, 0);
+          raw_v[j] = __builtin_amdgcn_raw_buffer_load_b16(rs, voff, part_b + code_at + j * row_b, 0);
         else
           raw_v[j] = __builtin_amdgcn_raw_buffer_load_b32(rs, voff, part_b + code_at + j * row_b, 0);
       }
@@ -649,7 +660,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
       uint8_t* buf = lds[tile & 1];
       if (masked(tile + 1) && tid == 0) bad[(tile + 1) % 3] = 0;
       {
-        const h2 d = both(raw_ks), off = minus8(d);
+        const h2 d = both(raw_ks | none), off = minus8(d);
 #pragma unroll
         for (int w = 0; w < KW; ++w)
           *reinterpret_cast<h8*>(buf + kwrite + 16 * w) = key_operand(raw_k[w], d, off);
