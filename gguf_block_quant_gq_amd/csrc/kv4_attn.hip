@@ -882,13 +882,26 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
   for (int64_t i = blockIdx.x; i < rows; i += gridDim.x) {
     const int64_t bh = i / per;
     const int r = (int)(i - bh * per), b = (int)(bh / c.n_kv), kvh = (int)(bh - (int64_t)b * c.n_kv);
-    const SeqRows s = seq_rows(c, b);
-    if (r / a.group >= s.n) continue;
     const int64_t slot0 = bh * a.splits * per + r;
+    const SeqRows s = seq_rows(c, b);
+    // the first parts are requested along with the maxima
+    constexpr int kAhead = 4;
+    f32x4 v[kAhead];
+    float pm[kAhead], pl[kAhead];
+    const auto request = [&](int p0) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int p = p0 + k * GROUPS < a.splits ? p0 + k * GROUPS : a.splits - 1;
+        pm[k] = ml[2 * (slot0 + p * per)], pl[k] = ml[2 * (slot0 + p * per) + 1];
+        v[k] = *reinterpret_cast<const f32x4*>(a.part + (slot0 + p * per) * c.hd + (on ? sub * 4 : 0));
+      }
+    };
+    request(g);
     float M = -INFINITY;
     for (int p = tid; p < a.splits; p += kThreads) M = fmaxf(M, ml[2 * (slot0 + p * per)]);
 #pragma unroll
     for (int w = 32; w > 0; w /= 2) M = fmaxf(M, __shfl_xor(M, w));
+    if (r / a.group >= s.n) continue;  // (the parts of such a row were never written)
     if ((tid & 63) == 0) sm[tid >> 6] = M;
     __syncthreads();
 #pragma unroll
@@ -896,13 +909,14 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
     const float base = M == -INFINITY ? 0.f : M;
     float tot = 0.f;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int p = g; p < a.splits; p += GROUPS) {
-      const float pm = ml[2 * (slot0 + p * per)], pl = ml[2 * (slot0 + p * per) + 1];
-      const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + (slot0 + p * per) * c.hd + (on ? sub * 4 : 0));
-      const bool none = pm == -INFINITY && pl == 0.f;
-      const float f = __builtin_amdgcn_exp2f(pm - base);
-      if (!none) tot += f * pl, sum += f * v;
+    for (int p = g; p < a.splits; p += kAhead * GROUPS) {
+      if (p > g) request(p);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const bool none = p + k * GROUPS >= a.splits || (pm[k] == -INFINITY && pl[k] == 0.f);
+        const float f = __builtin_amdgcn_exp2f(pm[k] - base);
+        if (!none) tot += f * pl[k], sum += f * v[k];
+      }
     }
     so[g][sub] = sum;
     if (sub == 0) st[g] = tot;
