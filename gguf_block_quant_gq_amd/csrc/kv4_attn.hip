@@ -865,72 +865,99 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
   }
 }
 
-// The parts of a split row added up: a workgroup per row, LANES = head_dim / 4
-// lanes (rounded up to a power of two) per part, so that 1024 / head_dim parts
-// are read at a time; then their sums in LDS, in a fixed order. Parts without
-// keys have a maximum of minus infinity and are skipped.
-template <int LANES>
+// The parts of a split row added up, in a fixed order. LANES = head_dim / 4
+// lanes (rounded up to a power of two) read a part. WHOLE: the workgroup's
+// groups of lanes share a row, group g taking parts g, g + GROUPS, ..., and
+// their sums meet in LDS (rows of many parts: a decode step has few rows);
+// else a group has a row to itself (rows of few parts: a prompt chunk has many
+// rows; 32768 rows of two parts took 61 us with a workgroup each). Parts
+// without keys have a maximum of minus infinity and are skipped.
+template <int LANES, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
-  constexpr int GROUPS = kThreads / LANES;
-  __shared__ f32x4 so[GROUPS][LANES];
+  constexpr int GROUPS = kThreads / LANES, STEP = WHOLE ? GROUPS : 1, kAhead = 4;
+  __shared__ f32x4 so[WHOLE ? GROUPS : 1][LANES];
   __shared__ float st[GROUPS], sm[kWaves];
   const Kv4Args& c = a.c;
   const int tid = threadIdx.x, sub = tid % LANES, g = tid / LANES;
   const int64_t per = (int64_t)a.max_q * a.group, rows = (int64_t)c.n_seq * c.n_kv * per;
   const float* ml = a.part + rows * a.splits * c.hd;
   const bool on = sub * 4 < c.hd;
-  for (int64_t i = blockIdx.x; i < rows; i += gridDim.x) {
+  const int64_t stride = (int64_t)gridDim.x * (WHOLE ? 1 : GROUPS);
+  for (int64_t i0 = (int64_t)blockIdx.x * (WHOLE ? 1 : GROUPS); i0 < rows; i0 += stride) {
+    const int64_t i = WHOLE ? i0 : i0 + g < rows ? i0 + g : rows - 1;
     const int64_t bh = i / per;
     const int r = (int)(i - bh * per), b = (int)(bh / c.n_kv), kvh = (int)(bh - (int64_t)b * c.n_kv);
     const int64_t slot0 = bh * a.splits * per + r;
     const SeqRows s = seq_rows(c, b);
     // the first parts are requested along with the maxima
-    constexpr int kAhead = 4;
+    const int p_first = WHOLE ? g : 0;
     f32x4 v[kAhead];
     float pm[kAhead], pl[kAhead];
     const auto request = [&](int p0) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int p = p0 + k * GROUPS < a.splits ? p0 + k * GROUPS : a.splits - 1;
+        const int p = p0 + k * STEP < a.splits ? p0 + k * STEP : a.splits - 1;
         pm[k] = ml[2 * (slot0 + p * per)], pl[k] = ml[2 * (slot0 + p * per) + 1];
         v[k] = *reinterpret_cast<const f32x4*>(a.part + (slot0 + p * per) * c.hd + (on ? sub * 4 : 0));
       }
     };
-    request(g);
+    request(p_first);
     float M = -INFINITY;
-    for (int p = tid; p < a.splits; p += kThreads) M = fmaxf(M, ml[2 * (slot0 + p * per)]);
+    const bool valid = r / a.group < s.n && (WHOLE || i0 + g < rows);  // (else the parts were never written)
+    if constexpr (WHOLE) {
+      for (int p = tid; p < a.splits; p += kThreads) M = fmaxf(M, ml[2 * (slot0 + p * per)]);
 #pragma unroll
-    for (int w = 32; w > 0; w /= 2) M = fmaxf(M, __shfl_xor(M, w));
-    if (r / a.group >= s.n) continue;  // (the parts of such a row were never written)
-    if ((tid & 63) == 0) sm[tid >> 6] = M;
-    __syncthreads();
+      for (int w = 32; w > 0; w /= 2) M = fmaxf(M, __shfl_xor(M, w));
+      if (!valid) continue;  // the same for the whole workgroup
+      if ((tid & 63) == 0) sm[tid >> 6] = M;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm[w]);
+      for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm[w]);
+    } else {
+      for (int p = sub; p < a.splits; p += LANES) M = fmaxf(M, ml[2 * (slot0 + p * per)]);
+#pragma unroll
+      for (int w = LANES / 2; w > 0; w /= 2) M = fmaxf(M, __shfl_xor(M, w));
+    }
     const float base = M == -INFINITY ? 0.f : M;
     float tot = 0.f;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int p = g; p < a.splits; p += kAhead * GROUPS) {
-      if (p > g) request(p);
+    for (int p = p_first; p < a.splits; p += kAhead * STEP) {
+      if (p > p_first) request(p);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const bool none = p + k * GROUPS >= a.splits || (pm[k] == -INFINITY && pl[k] == 0.f);
+        const bool none = p + k * STEP >= a.splits || (pm[k] == -INFINITY && pl[k] == 0.f);
         const float f = __builtin_amdgcn_exp2f(pm[k] - base);
         if (!none) tot += f * pl[k], sum += f * v[k];
       }
     }
-    so[g][sub] = sum;
-    if (sub == 0) st[g] = tot;
-    __syncthreads();
-    if (g == 0 && on) {
-      float t = st[0];
+    if constexpr (WHOLE) {
+      so[g][sub] = sum;
+      if (sub == 0) st[g] = tot;
+      __syncthreads();
+      if (g == 0) {
+        tot = st[0];
 #pragma unroll
-      for (int k = 1; k < GROUPS; ++k) t += st[k], sum += so[k][sub];
-      const f32x4 o = t == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : sum / t;
+        for (int k = 1; k < GROUPS; ++k) tot += st[k], sum += so[k][sub];
+      }
+    }
+    if (valid && on && (!WHOLE || g == 0)) {
+      const f32x4 o = tot == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : sum / tot;
       float* out = a.out + (int64_t)(s.first + r / a.group) * a.out_stride + (int64_t)(kvh * a.group + r % a.group) * c.hd;
       __builtin_memcpy(__builtin_assume_aligned(out + sub * 4, 4), &o, 16);
     }
-    __syncthreads();
+    if constexpr (WHOLE) __syncthreads();
   }
+}
+
+template <int LANES>
+void launch_join(const AttnArgs& a, int64_t rows, hipStream_t s) {
+  constexpr int GROUPS = kThreads / LANES;
+  // a workgroup per row while the GPU takes them all at once (eight per CU)
+  if (rows <= 2048)
+    hipLaunchKernelGGL((attn_join_kernel<LANES, true>), dim3((unsigned)rows), dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_join_kernel<LANES, false>), dim3((unsigned)std::min<int64_t>((rows + GROUPS - 1) / GROUPS, 1 << 20)),
+                       dim3(kThreads), 0, s, a);
 }
 
 // Rows of a sequence and kv head up to which the row kernel is taken.
@@ -988,10 +1015,9 @@ hipError_t launch_kv4_attn(const AttnArgs& a, hipStream_t s) {
   }
   if (a.splits > 1) {
     const int64_t all = a.c.n_seq * (int64_t)a.c.n_kv * rows;
-    const dim3 wgs((unsigned)std::min<int64_t>(all, 1 << 20));
-    if (a.c.hd <= 64) hipLaunchKernelGGL(attn_join_kernel<16>, wgs, dim3(kThreads), 0, s, a);
-    else if (a.c.hd <= 128) hipLaunchKernelGGL(attn_join_kernel<32>, wgs, dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL(attn_join_kernel<64>, wgs, dim3(kThreads), 0, s, a);
+    if (a.c.hd <= 64) launch_join<16>(a, all, s);
+    else if (a.c.hd <= 128) launch_join<32>(a, all, s);
+    else launch_join<64>(a, all, s);
   }
   return hipGetLastError();
 }
