@@ -611,6 +611,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
     const int tok = row_on ? row / a.group : 0;
     const int head = kvh * a.group + (row_on ? row - tok * a.group : 0);
     const Seen mine = seen_keys(a, pos0 + tok, len);
+    const bool wave_on = row0 + wave * 32 < R;  // else the wave only brings keys and values in
 
     typename RowTile<D>::Codes raw_v[4];
     uint32_t raw_k[KW], none = 0;
@@ -754,6 +755,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
       // 32 keys at a time, which keeps the scores and weights in 32 registers
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
+        if (!wave_on) break;
         f32x16 sc;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -986,8 +988,12 @@ void launch_tiles(const AttnArgs& a, hipStream_t s) {
 //   - to fill the GPU: up to 512 workgroups, of at least 512 keys each for the
 //     row kernel (one sequence of 333 keys: 13.5 us whole, 18.5 in two) and
 //     256 for the tile kernel, whose workgroups are that much slower (64
-//     positions over 2048 keys: 31 us with 256, 38 with 512); more does not
-//     pay (65536 keys, 8 kv heads: 26.5 us with 512, 32.4 with 1024);
+//     positions over 2048 keys: 30 us with 256, 37 with 512); more does not
+//     pay (65536 keys, 8 kv heads: 26.5 us with 512, 32.4 with 1024; 512
+//     positions over 8192 keys: 139 us with 512, 153 with 1024), but for the
+//     tile kernel 768 in two parts of 1024 keys or more are better than 384
+//     (a prompt of 3000 tokens, 16 heads: 108 us against 130; 4 chunks of 128
+//     positions over 4096 keys: 86 against 83);
 //   - for the row kernel, to even out sequences of different lengths: up to
 //     2048 workgroups of at least 1024 keys (32 sequences of 8k to 16k keys:
 //     99.7 us with 2048, 105 with 1024, 117 with 512; 4 sequences: 22.6 us
@@ -996,7 +1002,8 @@ int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len) 
   if (n_seq <= 0 || rows <= 0) return 1;
   const bool few = rows <= kRowKernelRows;
   const int64_t base = n_seq * n_kv * (few ? 1 : (rows + kTileRows - 1) / kTileRows);
-  const int64_t fill = std::min((max_len + (few ? 511 : 255)) / (few ? 512 : 256), 512 / base);
+  const int64_t most = few || base > 384 || max_len < 2048 ? 512 / base : std::max<int64_t>(2, 512 / base);
+  const int64_t fill = std::min((max_len + (few ? 511 : 255)) / (few ? 512 : 256), most);
   const int64_t even = few ? std::min((max_len + 1023) / 1024, 2048 / base) : 1;
   return (int)std::max<int64_t>({1, fill, even});
 }
