@@ -137,7 +137,7 @@ __device__ __forceinline__ RowScale row_scale(float largest, float scale) {
 
 // ---------------------------------------------------------- the row kernel --
 // Few rows a sequence (single tokens, or a few, times the query heads that
-// share a kv head: at most 16). A wave takes 32 keys at a time on its own: its
+// share a kv head: at most 32). A wave takes 32 keys at a time on its own: its
 // lanes read their keys' codes and scales straight into the places where the
 // matrix operands need them, the next tile's loads in flight while this one
 // is computed, and no LDS is used until the waves' sums are added at the end.
@@ -147,9 +147,10 @@ __device__ __forceinline__ RowScale row_scale(float largest, float scale) {
 //   the eight keys whose weights it holds (4 g .. 4 g + 3 of each half tile).
 //   Pairs of keys are put side by side by two byte permutes; channel i of
 //   every lane makes matrix tile i.
-// FUSED: at most 8 rows. Columns 0 .. 7 of the query operand hold hi parts and
-// 8 .. 15 the lo parts of the same rows, so one product gives both, one lane
-// rotation adds them, and likewise for the weights.
+// ROWS = 8 (FUSED): columns 0 .. 7 of the query operand hold hi parts and 8 ..
+// 15 the lo parts of the same rows, so one product gives both, one lane
+// rotation adds them, and likewise for the weights. ROWS = 32: two column
+// groups (NG) share the dequantised keys and values.
 // Bound: HBM. 144 bytes a token and kv head of 128 channels against about
 // 1500 cycles of issue per 32 keys and SIMD, an issue limit near 7 TB/s.
 template <int D>
@@ -166,22 +167,27 @@ struct RowTile {
   u32x2 vs[2];
 };
 
-template <int D, bool FUSED>
-__global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn_rows_kernel(AttnArgs a) {
+constexpr int row_kernel_waves(int d, int rows) {  // per SIMD: what the registers allow
+  return rows == 32 ? (d == 64 ? 3 : d == 128 ? 2 : 1) : d == 64 ? 4 : d == 128 ? 3 : 2;
+}
+
+template <int D, int ROWS>
+__global__ __launch_bounds__(kThreads, row_kernel_waves(D, ROWS)) void attn_rows_kernel(AttnArgs a) {
   typedef RowTile<D> Tile;
+  constexpr bool FUSED = ROWS == 8;
+  constexpr int NG = ROWS == 32 ? 2 : 1;
   constexpr int KW = Tile::KW, VW = Tile::VW, NT = D / 16;  // NT: matrix tiles of channels
-  constexpr int ROWS = FUSED ? 8 : 16;
   constexpr int PASS = ROWS * D > 2048 ? ROWS * D / 2048 : 1;  // the waves' sums meet in 32 KB of LDS
   constexpr int TP = NT / PASS;
   __shared__ float so[kWaves][ROWS][TP * 16 + 4];
-  __shared__ float sm[kWaves][16], sl[kWaves][16];
+  __shared__ float sm[kWaves][16 * NG], sl[kWaves][16 * NG];
 
   const Kv4Args& c = a.c;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15, g = lane >> 4;
   const int kvh = blockIdx.x % c.n_kv, split = blockIdx.x / c.n_kv;
   const int hd = c.hd, lg = c.page_log2, P = 1 << lg;
-  const int row = FUSED ? (m & 7) : m;
+  const int row = FUSED ? (m & 7) : m;  // and 16 further on
 
   // lane constants: offsets inside a key part and a value part of a page
   const int row_b = hd / 2;
@@ -212,8 +218,9 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn
     // the first and last rows' keys bound everyone's
     const int pos0 = len - s.n;
     const Seen first = seen_keys(a, pos0, len), last = seen_keys(a, pos0 + n - 1, len);
-    const int t = s.first + row / a.group;
-    const Seen mine = seen_keys(a, pos0 + row / a.group, len);
+    Seen mine[NG];
+#pragma unroll
+    for (int q = 0; q < NG; ++q) mine[q] = seen_keys(a, pos0 + (row + 16 * q) / a.group, len);
     const int lo = first.lo & ~(kTile - 1), hi = last.hi;
     const int tiles = hi > first.lo ? (hi - lo + kTile - 1) / kTile : 0;
     const int parts = a.splits * kWaves, mypart = split * kWaves + wave;
@@ -224,14 +231,16 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn
     // the query operand: lane (m, g) holds the channels that its key lanes
     // hold, of row m (FUSED: the hi part of row m, or the lo part of row m - 8);
     // loaded first, and made operands with the first tile's loads in flight
-    const bool q_on = row < R;
-    const float* qr = a.q + (int64_t)(q_on ? t : s.first) * a.q_stride +
-                      (int64_t)(kvh * a.group + (q_on ? row % a.group : 0)) * hd;
-    f32x4 qx[KW][2];
+    f32x4 qx[NG][KW][2];
 #pragma unroll
-    for (int w = 0; w < KW; ++w) {
-      const int c0 = (g * KW + w) * 8, at = c0 < hd ? c0 : 0;
-      qx[w][0] = load_f32x4(qr + at), qx[w][1] = load_f32x4(qr + at + 4);
+    for (int q = 0; q < NG; ++q) {
+      const int r = row + 16 * q < R ? row + 16 * q : 0;
+      const float* qr = a.q + (int64_t)(s.first + r / a.group) * a.q_stride + (int64_t)(kvh * a.group + r % a.group) * hd;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const int c0 = (g * KW + w) * 8, at = c0 < hd ? c0 : 0;
+        qx[q][w][0] = load_f32x4(qr + at), qx[q][w][1] = load_f32x4(qr + at + 4);
+      }
     }
 
     const int32_t* table = c.table + (int64_t)b * c.table_stride;
@@ -294,44 +303,50 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn
       load_values(begin, id0, id1);
     }
 
-    h8 qh[KW], ql[FUSED ? 1 : KW];
-    float down;
-    {
+    h8 qh[NG][KW], ql[NG][FUSED ? 1 : KW];
+    float down[NG];
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
       float big = 0.f;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        const bool in = q_on && (g * KW + w) * 8 < hd;
+        const bool in = row + 16 * q < R && (g * KW + w) * 8 < hd;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          qx[w][i >> 2][i & 3] = in ? qx[w][i >> 2][i & 3] : 0.f;
-          big = fmaxf(big, __builtin_fabsf(qx[w][i >> 2][i & 3]));
+          const float y = in ? qx[q][w][i >> 2][i & 3] : 0.f;
+          qx[q][w][i >> 2][i & 3] = y;
+          big = fmaxf(big, __builtin_fabsf(y));
         }
       }
       const RowScale rs = row_scale(max_over_rows(big), a.scale);
-      down = rs.down;
+      down[q] = rs.down;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
         h8 h, l;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int e = slot_channel(j);
-          const float y = qx[w][e >> 2][e & 3] * rs.up;
+          const float y = qx[q][w][e >> 2][e & 3] * rs.up;
           h[j] = (_Float16)y;
           l[j] = (_Float16)(y - (float)h[j]);
         }
         if constexpr (FUSED) {
-          qh[w] = m < 8 ? h : l;
+          qh[q][w] = m < 8 ? h : l;
         } else {
-          qh[w] = h;
-          ql[w] = l;
+          qh[q][w] = h;
+          ql[q][w] = l;
         }
       }
     }
 
-    f32x4 o[NT];
+    f32x4 o[NG][NT];
+    float mx[NG], l[NG];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float mx = -INFINITY, l = 0.f;
+    for (int q = 0; q < NG; ++q) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o[q][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      mx[q] = -INFINITY, l[q] = 0.f;
+    }
 
     // Keys and values have one set of registers each: the next tile's keys are
     // requested when this tile's have been multiplied, its values likewise, and
@@ -343,18 +358,22 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn
       const int next = key0 + kTile < end ? key0 + kTile : key0;
       const int jd0 = page_id(next), jd1 = page_id(next + 16);
       // scores: rows are this half tile's keys 4 g + r, columns query rows
-      f32x4 sc[2];
+      f32x4 sc[NG][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         __builtin_amdgcn_sched_barrier(0);
-        sc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < NG; ++q) sc[q][u] = f32x4{0.f, 0.f, 0.f, 0.f};
         const uint32_t none = page_ok(u ? id1 : id0) ? 0u : 0x7E00u;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
           const h2 d = both(x.ks[u][w / 4] | none);
           const h8 k = key_operand(x.k[u][w], d, minus8(d));
-          sc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[w], sc[u], 0, 0, 0);
-          if constexpr (!FUSED) sc[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[w], sc[u], 0, 0, 0);
+#pragma unroll
+          for (int q = 0; q < NG; ++q) {
+            sc[q][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[q][w], sc[q][u], 0, 0, 0);
+            if constexpr (!FUSED) sc[q][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[q][w], sc[q][u], 0, 0, 0);
+          }
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -364,7 +383,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) sc[u][r] += dpp_f32<0x128>(sc[u][r]);  // row_ror:8: hi + lo
+          for (int r = 0; r < 4; ++r) sc[0][u][r] += dpp_f32<0x128>(sc[0][u][r]);  // row_ror:8: hi + lo
       }
       // masks, in tiles that reach past some row's keys. There a value whose
       // scale is not finite must not meet the zero weight of a row that does
@@ -389,40 +408,47 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int key = key0 + 16 * u + 4 * g + r;
-            if (bad >> (4 * u + r) & 1) sc[u][r] = __builtin_nanf("");
-            if (key < mine.lo || key >= mine.hi) sc[u][r] = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < NG; ++q) {
+              if (bad >> (4 * u + r) & 1) sc[q][u][r] = __builtin_nanf("");
+              if (key < mine[q].lo || key >= mine[q].hi) sc[q][u][r] = -INFINITY;
+            }
           }
         }
       }
-      float top = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
-                        fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3])));
-      top = max_over_rows(top) * down;
-      if (__any(top > mx + kSlack)) {
-        const float nm = fmaxf(mx, top);
-        const float f = __builtin_amdgcn_exp2f(mx - (nm == -INFINITY ? 0.f : nm));
-        mx = nm;
-        l *= f;
+      h8 wl[NG], wh[NG];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) o[i] *= f;
-      }
-      const float base = mx == -INFINITY ? 0.f : mx;
-      const float part = FUSED && m < 8 ? 0.f : -1.f;
-      h2 ph[4], pl[4];
+      for (int q = 0; q < NG; ++q) {
+        float top = fmaxf(fmaxf(fmaxf(sc[q][0][0], sc[q][0][1]), fmaxf(sc[q][0][2], sc[q][0][3])),
+                          fmaxf(fmaxf(sc[q][1][0], sc[q][1][1]), fmaxf(sc[q][1][2], sc[q][1][3])));
+        top = max_over_rows(top) * down[q];
+        if (__any(top > mx[q] + kSlack)) {
+          const float nm = fmaxf(mx[q], top);
+          const float f = __builtin_amdgcn_exp2f(mx[q] - (nm == -INFINITY ? 0.f : nm));
+          mx[q] = nm;
+          l[q] *= f;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int r = 0; r < 4; r += 2) {
-          const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][r], down, -base));
-          const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[u][r + 1], down, -base));
-          l += p0 + p1;
-          // (FUSED: p itself in the hi columns)
-          ph[2 * u + r / 2] = hi_parts(p0, p1);
-          pl[2 * u + r / 2] = lo_parts(ph[2 * u + r / 2], p0, p1, part);
+          for (int i = 0; i < NT; ++i) o[q][i] *= f;
         }
+        const float base = mx[q] == -INFINITY ? 0.f : mx[q];
+        const float part = FUSED && m < 8 ? 0.f : -1.f;
+        h2 ph[4], pl[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) {
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][u][r], down[q], -base));
+            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][u][r + 1], down[q], -base));
+            l[q] += p0 + p1;
+            // (FUSED: p itself in the hi columns)
+            ph[2 * u + r / 2] = hi_parts(p0, p1);
+            pl[2 * u + r / 2] = lo_parts(ph[2 * u + r / 2], p0, p1, part);
+          }
+        }
+        wl[q] = as_h8(pl[0], pl[1], pl[2], pl[3]);
+        wh[q] = as_h8(ph[0], ph[1], ph[2], ph[3]);
       }
       __builtin_amdgcn_sched_barrier(0);
-      const h8 wl = as_h8(pl[0], pl[1], pl[2], pl[3]);
-      const h8 wh = as_h8(ph[0], ph[1], ph[2], ph[3]);
       // values: pairs of keys side by side, channel by channel
       h2 vd[4], voffs[4];
 #pragma unroll
@@ -447,8 +473,11 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn
           // channels lie in the low half of a dword, odd ones in the high
           const auto tile = [&](int i, h8 v) {
             const int at = D == 64 ? i : w * 8 + 2 * i + half;
-            o[at] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, wl, o[at], 0, 0, 0);
-            if constexpr (!FUSED) o[at] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, wh, o[at], 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < NG; ++q) {
+              o[q][at] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, wl[q], o[q][at], 0, 0, 0);
+              if constexpr (!FUSED) o[q][at] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, wh[q], o[q][at], 0, 0, 0);
+            }
           };
           tile(0, as_h8(two_values<0>(lo4[0], vd[0], voffs[0]), two_values<0>(lo4[1], vd[1], voffs[1]),
                         two_values<0>(lo4[2], vd[2], voffs[2]), two_values<0>(lo4[3], vd[3], voffs[3])));
@@ -464,15 +493,22 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn
       id0 = jd0, id1 = jd1;
       load_values(next, id0, id1);
     }
-    l = sum_over_rows(l);
 
     // the waves' sums, in wave order
-    if (g == 0) sm[wave][m] = mx, sl[wave][m] = l;
-    __syncthreads();
-    float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm[w][m]);
-    const float f = __builtin_amdgcn_exp2f(mx - (M == -INFINITY ? 0.f : M));
+    for (int q = 0; q < NG; ++q) {
+      l[q] = sum_over_rows(l[q]);
+      if (g == 0) sm[wave][16 * q + m] = mx[q], sl[wave][16 * q + m] = l[q];
+    }
+    __syncthreads();
+    float f[NG];
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm[w][16 * q + m]);
+      f[q] = __builtin_amdgcn_exp2f(mx[q] - (M == -INFINITY ? 0.f : M));
+    }
     const int64_t slot0 = (((int64_t)b * c.n_kv + kvh) * a.splits + split) * ((int64_t)a.max_q * a.group);
     float* ml = a.part + (int64_t)c.n_seq * c.n_kv * a.splits * a.max_q * a.group * hd;
     for (int p = 0; p < PASS; ++p) {
@@ -480,15 +516,18 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 3 : 2) void attn
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         if (i / TP == p) {
-          f32x4 v = o[i];
-          if constexpr (FUSED) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] += dpp_f32<0x128>(v[r]);
-          }
-          v *= f;
-          if (!FUSED || m < 8) {
+          for (int q = 0; q < NG; ++q) {
+            f32x4 v = o[q][i];
+            if constexpr (FUSED) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) so[wave][row][(4 * g + r) * TP + i % TP] = v[r];
+              for (int r = 0; r < 4; ++r) v[r] += dpp_f32<0x128>(v[r]);
+            }
+            v *= f[q];
+            if (!FUSED || m < 8) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) so[wave][row + 16 * q][(4 * g + r) * TP + i % TP] = v[r];
+            }
           }
         }
       }
@@ -963,14 +1002,16 @@ void launch_join(const AttnArgs& a, int64_t rows, hipStream_t s) {
 }
 
 // Rows of a sequence and kv head up to which the row kernel is taken.
-constexpr int kRowKernelRows = 16;
+constexpr int kRowKernelRows = 32;
 
 template <int D>
-void launch_rows(const AttnArgs& a, bool fused, hipStream_t s) {
+void launch_rows(const AttnArgs& a, hipStream_t s) {
+  const int64_t rows = (int64_t)a.max_q * a.group;
   const int64_t gx = (int64_t)a.c.n_kv * a.splits;
   const dim3 grid((unsigned)gx, (unsigned)std::max<int64_t>(1, std::min<int64_t>(a.c.n_seq, (1 << 22) / gx)));
-  if (fused) hipLaunchKernelGGL((attn_rows_kernel<D, true>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((attn_rows_kernel<D, false>), grid, dim3(kThreads), 0, s, a);
+  if (rows <= 8) hipLaunchKernelGGL((attn_rows_kernel<D, 8>), grid, dim3(kThreads), 0, s, a);
+  else if (rows <= 16) hipLaunchKernelGGL((attn_rows_kernel<D, 16>), grid, dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((attn_rows_kernel<D, 32>), grid, dim3(kThreads), 0, s, a);
 }
 
 template <int D>
@@ -1011,10 +1052,9 @@ int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len) 
 hipError_t launch_kv4_attn(const AttnArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.max_q * a.group;
   if (rows <= kRowKernelRows) {
-    const bool fused = rows <= 8;
-    if (a.c.hd <= 64) launch_rows<64>(a, fused, s);
-    else if (a.c.hd <= 128) launch_rows<128>(a, fused, s);
-    else launch_rows<256>(a, fused, s);
+    if (a.c.hd <= 64) launch_rows<64>(a, s);
+    else if (a.c.hd <= 128) launch_rows<128>(a, s);
+    else launch_rows<256>(a, s);
   } else {
     if (a.c.hd <= 64) launch_tiles<64>(a, s);
     else if (a.c.hd <= 128) launch_tiles<128>(a, s);

@@ -35,6 +35,13 @@ def queries(b, heads, size=1.0):
     ([2, 0, 3], [100, 7, 3], 16, 4, 2, 64, True, 0),
     ([4], [500], 32, 8, 2, 128, True, 0),
     ([3, 2], [40, 90], 16, 4, 2, 96, False, 0),
+    # 17 to 32 rows of a sequence and kv head, and one more
+    ([8], [500], 32, 8, 2, 128, True, 0),
+    ([3, 1, 0], [90, 17, 0], 16, 14, 2, 64, True, 0),
+    ([6, 2], [100, 7], 16, 10, 2, 256, True, 0),
+    ([5, 4], [60, 333], 16, 8, 2, 96, True, 21),
+    ([32], [70], 16, 2, 2, 128, False, 0),
+    ([33], [70], 16, 2, 2, 128, False, 0),
     # prompts: whole, chunks, ragged, odd
     ([33], [33], 16, 2, 1, 64, True, 0),
     ([100, 65, 1], [100, 200, 70], 16, 4, 2, 128, True, 0),
@@ -61,12 +68,13 @@ def test_against_oracle(gq, n, lens, P, H, n_kv, hd, causal, window):
     print(f"[kv4] {worst:.3f} of the bound", flush=True)
 
 
-@pytest.mark.parametrize("n,lens", [([1], [9000]), ([1, 1, 1], [5000, 1, 3001]), ([3], [4097]), ([64], [4500])])
+@pytest.mark.parametrize("n,lens", [([1], [9000]), ([1, 1, 1], [5000, 1, 3001]), ([3], [4097]), ([7, 5], [4097, 900]),
+                                    ([64], [4500])])
 def test_long_contexts(gq, n, lens):
     # long enough to be cut into parts, with several lengths under one bound
     b = Batch(sum(lens), n, lens, 64, 2, 128)
     q = queries(b, 8)
-    rows = None if b.n_tok < 8 else [0, 1, 31, 32, 63]
+    rows = None if b.n_tok < 13 else [0, 1, 31, 32, 63]
     for max_len in (max(lens), b.table.shape[1] * 64):
         out = to_host(run(gq, b, q, max_len=max_len))
         check_attention(b, out, q, 128 ** -0.5, True, 0, rows=rows)
@@ -116,7 +124,7 @@ def test_rows_that_see_nothing_and_rows_of_none(gq):
         check_attention(b, got, q[:b.n_tok], 64 ** -0.5, True, 0, rows=rows)
 
 
-@pytest.mark.parametrize("n", [[1, 1], [3, 2], [40, 37]])
+@pytest.mark.parametrize("n", [[1, 1], [3, 2], [9, 10], [40, 37]])
 def test_nan_in_unwritten_slots(gq, n):
     """Slots past the length hold NaN scales; so do spare pages."""
     b = Batch(80, n, [50, 37], 16, 2, 64)
@@ -139,7 +147,7 @@ def test_nan_in_unwritten_slots(gq, n):
 
 @pytest.mark.parametrize("kv", [0, 1])
 @pytest.mark.parametrize("bits", [0x7E00, 0x7C00])
-@pytest.mark.parametrize("n,lens,window", [([6], [50], 0), ([60], [60], 0), ([60], [130], 20), ([2], [100], 9)])
+@pytest.mark.parametrize("n,lens,window", [([6], [50], 0), ([12], [50], 0), ([60], [60], 0), ([60], [130], 20), ([2], [100], 9)])
 def test_nan_in_a_seen_key_reaches_only_rows_that_see_it(gq, n, lens, window, kv, bits):
     b = Batch(81, n, lens, 16, 1, 64)
     clean = b.pages.copy()
@@ -163,7 +171,7 @@ def test_nan_in_a_seen_key_reaches_only_rows_that_see_it(gq, n, lens, window, kv
         assert (~np.isfinite(out[sees][..., 32:])).any()
 
 
-@pytest.mark.parametrize("n", [[1], [5], [50]])
+@pytest.mark.parametrize("n", [[1], [5], [15], [50]])
 def test_page_numbers_that_are_none(gq, n):
     # pages 1 and 2 of the sequence: NaN for the rows that see them, no fault
     b = Batch(82, n, [60], 16, 2, 64)
