@@ -101,31 +101,39 @@ __device__ __forceinline__ SeqRows seq_rows(const Kv4Args& c, int b) {
 }
 
 // The position of token row t, and its sequence; -1 where the row belongs to
-// none. The offsets are searched 64 at a time (one load per lane and a
-// ballot), so a batch of up to 64 sequences costs one round trip.
+// none. Called by whole waves. The offsets are searched 64 at a time (one load
+// per lane and a ballot) with the lengths alongside, so a batch of up to 63
+// sequences costs one round trip.
 __device__ __forceinline__ int row_position(const Kv4Args& c, int t, int* seq) {
   int b = t;
+  int64_t first = t, end = (int64_t)t + 1, len;
   if (c.q_start) {
-    // the last b with q_start[b] <= t
+    // the last b with q_start[b] <= t, among the n offsets from lo on
     const int lane = threadIdx.x & 63;
     int lo = 0, n = c.n_seq + 1;
-    while (n > 1) {
-      const int step = (n + 63) / 64;
-      const int i = lo + lane * step;
-      const uint64_t m = __ballot(lane * step < n && c.q_start[i < c.n_seq ? i : c.n_seq] <= t);
+    for (;;) {
+      const int step = (n + 63) / 64, i = lo + lane * step;
+      const int start = c.q_start[i < c.n_seq ? i : c.n_seq];
+      const int l = c.lens[i < c.n_seq ? i : c.n_seq - 1];
+      const uint64_t m = __ballot(lane * step < n && start <= t);
       if (m == 0) return -1;
       const int at = 63 - __clzll((unsigned long long)m);
-      const int end = lo + n;
+      if (step == 1) {
+        b = lo + at;
+        if (b >= c.n_seq) return -1;
+        first = __shfl(start, at), len = __shfl(l, at);
+        end = at < 63 ? __shfl(start, at + 1) : c.q_start[b + 1];
+        break;
+      }
+      const int stop = lo + n;
       lo += at * step;
-      n = step < end - lo ? step : end - lo;
+      n = step < stop - lo ? step : stop - lo;
     }
-    b = lo;
+  } else {
+    len = c.lens[b];
   }
-  if (b >= c.n_seq) return -1;
-  const SeqRows s = seq_rows(c, b);
-  const int64_t i = (int64_t)t - s.first;
-  if (i < 0 || i >= s.n) return -1;
-  const int64_t p = (int64_t)s.len - s.n + i;
+  if (first < 0 || end > c.n_tok || t < first || t >= end) return -1;
+  const int64_t p = len - (end - t);
   if (p < 0 || p >= ((int64_t)c.table_stride << c.page_log2)) return -1;
   *seq = b;
   return (int)p;

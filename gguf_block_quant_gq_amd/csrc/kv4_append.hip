@@ -177,6 +177,7 @@ __global__ __launch_bounds__(kThreads) void qk_rope_kernel(QkArgs a) {
   __shared__ uint8_t* pages[TOK];
   __shared__ int where[TOK];           // positions; -1: the row belongs to none
   constexpr int kHeads = kThreads / GL;  // heads per pass
+  static_assert(TOK <= kThreads / 64, "a wave looks up each token");
   const int tid = threadIdx.x, sub = tid % GL, slot = tid / GL;
   const int hd = a.hd, c0 = sub * 8, half = a.r.half;
   const bool lane_on = c0 < hd;
@@ -230,11 +231,14 @@ __global__ __launch_bounds__(kThreads) void qk_rope_kernel(QkArgs a) {
       if (first) {  // the angles, with the loads above in flight
         first = false;
         __syncthreads();  // the tokens before have been turned
+        uint8_t* page = nullptr;
+        const int mine = tid >> 6;  // the token that this wave looks up (TOK is at most the waves)
         if constexpr (APPEND) {
-          for (int k = tid >> 6; k < toks; k += kThreads / 64) {
+          if (mine < toks) {
             int seq = 0;
-            const int p = row_position(a.c, t0 + k, &seq);
-            if ((tid & 63) == 0) where[k] = p, pages[k] = p < 0 ? nullptr : page_of(a.c, seq, p);
+            const int p = row_position(a.c, t0 + mine, &seq);
+            if ((tid & 63) == 0) where[mine] = p;
+            if (p >= 0) page = page_of(a.c, seq, p);  // arrives under the angles
           }
           __syncthreads();
         }
@@ -245,6 +249,7 @@ __global__ __launch_bounds__(kThreads) void qk_rope_kernel(QkArgs a) {
             turn[k][p] = sin_cos((double)pos * (double)a.r.freqs[p]) * (double)a.r.mscale;
           }
         }
+        if (APPEND && mine < toks && (tid & 63) == 0) pages[mine] = page;
         __syncthreads();
       }
 #pragma unroll
