@@ -791,28 +791,41 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
     for (int tile = tile0; tile < tile1; ++tile) {
       const uint8_t* buf = lds[tile & 1];
       const int key0 = lo + tile * KT;
-      // 32 keys at a time, which keeps the scores and weights in 32 registers
+      // 32 keys at a time, which keeps the scores and weights in 32 registers.
+      // An operand is asked for in LDS one product ahead, the first one of the
+      // values before the softmax (a prompt of 4096 positions, 32 heads: 440 -> 420 us).
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
         if (!wave_on) break;
-        f32x16 sc;
+        f32x16 sc = {};
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) sc[r] = 0.f;
+        const uint8_t* kb = buf + kread + 32 * k * C::KROW;
+        h8 x = *reinterpret_cast<const h8*>(kb);
 #pragma unroll
         for (int w = 0; w < KS; ++w) {
-          const h8 x = *reinterpret_cast<const h8*>(buf + kread + 32 * k * C::KROW + 32 * w);
+          h8 y;
+          if (w + 1 < KS) y = *reinterpret_cast<const h8*>(kb + 32 * (w + 1));
+          __builtin_amdgcn_sched_barrier(0);
           sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, qh[w], sc, 0, 0, 0);
           sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, ql[w], sc, 0, 0, 0);
+          x = y;
+          __builtin_amdgcn_sched_barrier(0);
         }
+        const auto v_at = [&](int u) {
+          return *reinterpret_cast<const h8*>(buf + vread + 32 * (u % NT) * C::VROW + 32 * (2 * k + u / NT));
+        };
+        x = v_at(0);
         __builtin_amdgcn_sched_barrier(0);
         if (masked(tile)) {
-          const unsigned long long bm = bad[tile % 3];
+          // (keys counted from the lane's first one, so that all that differs
+          // between its scores are constants)
+          const uint32_t bm = (uint32_t)(bad[tile % 3] >> (32 * k)) >> (4 * h);
+          const int from = mine.lo - (key0 + 32 * k + 4 * h), to = mine.hi - (key0 + 32 * k + 4 * h);
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            const int at = 32 * k + 8 * (r >> 2) + 4 * h + (r & 3), key = key0 + at;
+            const int at = 8 * (r >> 2) + (r & 3);
             if (bm >> at & 1) sc[r] = __builtin_nanf("");
-            if (key < mine.lo || key >= mine.hi) sc[r] = -INFINITY;
+            if (at < from || at >= to) sc[r] = -INFINITY;
           }
         }
         float top = sc[0];
@@ -850,13 +863,14 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const h8 x = *reinterpret_cast<const h8*>(buf + vread + 32 * i * C::VROW + 32 * (2 * k + t));
-            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, ph[t], o[i], 0, 0, 0);
-            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, pl[t], o[i], 0, 0, 0);
-          }
+        for (int u = 0; u < 2 * NT; ++u) {
+          h8 y;
+          if (u + 1 < 2 * NT) y = v_at(u + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          o[u % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, ph[u / NT], o[u % NT], 0, 0, 0);
+          o[u % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, pl[u / NT], o[u % NT], 0, 0, 0);
+          x = y;
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
