@@ -534,7 +534,7 @@ class Rope:
 
     def __init__(self, freqs, interleaved: bool = False, mscale: float = 1.0):
         _check_dev(freqs, "freqs", _torch().float32)
-        self.freqs, self.rot = freqs, 2 * freqs.numel()
+        self.freqs, self.rot, self._dev = freqs, 2 * freqs.numel(), freqs.get_device()
         self.interleaved, self.mscale = bool(interleaved), float(mscale)
         self._struct = _RopeStruct(_ptr(freqs), self.rot, int(self.interleaved), self.mscale)
         self._ref = ctypes.addressof(self._struct)
@@ -557,7 +557,7 @@ class KV4Cache:
             raise GQError(GQ_ERR_SHAPE, "KV4Cache")
         if pages.numel() % self.page_bytes:
             raise ValueError(f"pages must hold whole pages of {self.page_bytes} bytes")
-        self.pages, self.table = pages, table
+        self.pages, self.table, self._dev = pages, table, pages.get_device()
         self.n_pages = pages.numel() // self.page_bytes
         self.page_tokens, self.n_kv, self.head_dim = int(page_tokens), int(n_kv), int(head_dim)
         self.n_seq, self.capacity = table.shape[0], table.shape[1] * self.page_tokens
@@ -578,15 +578,24 @@ def _heads(t, name, dev):
         raise TypeError(f"{name} must be a torch tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current device, cuda:{dev}")
-    if t.dtype != torch.float32:
+    if t.dtype is not torch.float32:
         raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    n, h, d = t.shape
+    n, h, d = shape
     st, sh, sd = t.stride()
     if (d > 1 and sd != 1) or (h > 1 and sh != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return st if n > 1 else h * d
+
+
+def _new(x, shape, stream, dtype=None):
+    """A tensor on x's device from the pool of the stream that fills it."""
+    if stream is None:
+        return x.new_empty(shape, dtype=dtype)
+    with _torch().cuda.stream(stream):
+        return x.new_empty(shape, dtype=dtype)
 
 
 def _flat(t, name, dtype, n, dev):
@@ -597,7 +606,7 @@ def _flat(t, name, dtype, n, dev):
         raise TypeError(f"{name} must be a torch tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current device, cuda:{dev}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -611,7 +620,7 @@ def _rope_ref(rope, dev):
         return None
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a Rope")
-    if rope.freqs.get_device() != dev:
+    if rope._dev != dev:
         raise ValueError(f"rope must be on the current device, cuda:{dev}")
     return rope._ref
 
@@ -621,7 +630,7 @@ def _batch(cache, lens, q_start, n_tok, dev):
     torch = _torch()
     if not isinstance(cache, KV4Cache):
         raise TypeError("cache must be a KV4Cache")
-    if cache.pages.get_device() != dev:
+    if cache._dev != dev:
         raise ValueError(f"cache must be on the current device, cuda:{dev}")
     if q_start is None and n_tok != cache.n_seq:
         raise ValueError("without q_start there is one row per sequence")
@@ -638,10 +647,11 @@ def gq_qk_rope(x, pos, rope=None, norm=None, eps: float = 1e-6, out=None, stream
     xs = _heads(x, "x", dev)
     n, h, d = x.shape
     if out is None:
-        out = x.new_empty((n, h, d))
-    os_ = _heads(out, "out", dev)
-    if out.shape != x.shape:
-        raise ValueError("out must have x's shape")
+        out, os_ = _new(x, x.shape, stream), h * d
+    else:
+        os_ = _heads(out, "out", dev)
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
     st = load_library().gq_qk_rope(x.data_ptr(), xs, n, h, d, _flat(pos, "pos", torch.int32, n, dev),
                                    _rope_ref(rope, dev), _flat(norm, "norm", torch.float32, d, dev),
                                    eps, out.data_ptr(), os_, _stream_handle(stream))
@@ -672,10 +682,11 @@ def gq_kv4_append(cache, k, v, lens, q_start=None, rope=None, k_norm=None, q=Non
         if q.shape[0] != n or q.shape[2] != d:
             raise ValueError(f"q must be [{n}, heads, {d}]")
         if q_out is None:
-            q_out = q.new_empty((n, heads, d))
-        qos = _heads(q_out, "q_out", dev)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
+            q_out, qos = _new(q, q.shape, stream), heads * d
+        else:
+            qos = _heads(q_out, "q_out", dev)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -697,9 +708,9 @@ def gq_kv4_read(cache, lens, n_tok: int, q_start=None, K=None, V=None, stream=No
     starts, lengths = _batch(cache, lens, q_start, n_tok, dev)
     shape = (n_tok, cache.n_kv, cache.head_dim)
     if K is None:
-        K = torch.empty(shape, dtype=torch.float32, device=cache.pages.device)
+        K = _new(cache.pages, shape, stream, torch.float32)
     if V is None:
-        V = torch.empty(shape, dtype=torch.float32, device=cache.pages.device)
+        V = _new(cache.pages, shape, stream, torch.float32)
     n = n_tok * cache.n_kv * cache.head_dim
     st = load_library().gq_kv4_read(cache._ref, n_tok, starts, lengths, _flat(K, "K", torch.float32, n, dev),
                                     _flat(V, "V", torch.float32, n, dev), _stream_handle(stream))
@@ -716,11 +727,13 @@ def gq_kv4_attn_ws_bytes(cache, n_head: int, max_q: int, max_len: int) -> int:
     return need
 
 
-def gq_kv4_attn(cache, q, lens, q_start=None, max_q: int = 1, max_len=None, scale=None, causal: bool = True,
+def gq_kv4_attn(cache, q, lens, q_start=None, max_q=None, max_len=None, scale=None, causal: bool = True,
                 window: int = 0, out=None, workspace=None, stream=None):
     """Attention of q [tokens, heads, head_dim] over the cache (head_dim ** -0.5
-    is the default scale, the table's capacity the default max_len). max_q is
-    at least every sequence's rows. workspace: a uint8 GPU tensor of
+    is the default scale, the table's capacity the default max_len). max_q: at
+    least every sequence's rows (default: what is always enough, 1 without
+    q_start and else all the tokens; a tight bound is faster). Rows of no
+    sequence are not written. workspace: a uint8 GPU tensor of
     gq_kv4_attn_ws_bytes that no other call in flight uses; None takes one
     from torch's allocator for this call on its stream. Asynchronous."""
     torch = _torch()
@@ -731,22 +744,21 @@ def gq_kv4_attn(cache, q, lens, q_start=None, max_q: int = 1, max_len=None, scal
     if d != cache.head_dim:
         raise ValueError(f"q must be [tokens, heads, {cache.head_dim}]")
     if out is None:
-        out = q.new_empty((n, heads, d))
-    os_ = _heads(out, "out", dev)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
+        out, os_ = _new(q, q.shape, stream), heads * d
+    else:
+        os_ = _heads(out, "out", dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
     if max_len is None:
         max_len = cache.capacity
+    if max_q is None:
+        max_q = 1 if q_start is None else n
     lib = load_library()
     need = lib.gq_kv4_attn_ws_bytes(cache._ref, heads, max_q, max_len)
     if need < 0:
         raise GQError(GQ_ERR_SHAPE, "gq_kv4_attn")
     if workspace is None and need > 0:
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        else:
-            with torch.cuda.stream(stream):  # freed into the stream that the kernels run on
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _new(cache.pages, (need,), stream)
     st = lib.gq_kv4_attn(cache._ref, q.data_ptr(), qs, heads, n, starts, lengths, max_q, max_len,
                          d ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(), os_,
                          _flat(workspace, "workspace", torch.uint8, need, dev),

@@ -18,8 +18,7 @@
 // value are lane exchanges, and a head may be turned in place (its loads all
 // precede its stores). A workgroup takes a token, or four where there are many:
 // their sines and cosines (about 60 fp64 operations a pair) are computed once
-// into LDS for all heads, with the first heads' loads in flight; from then on
-// the next pass's loads run under each pass's arithmetic.
+// into LDS for all heads, with the first heads' loads in flight.
 #include <algorithm>
 
 #include "gq_device.h"

@@ -1015,6 +1015,12 @@ void launch_join(const AttnArgs& a, int64_t rows, hipStream_t s) {
                        dim3(kThreads), 0, s, a);
 }
 
+// The grid's second extent: the sequences, up to 2^22 workgroups in all and
+// the extent that HIP allows on every device; a workgroup goes on to the next ones.
+unsigned sequences_at_once(const AttnArgs& a, int64_t gx) {
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>({a.c.n_seq, (1 << 22) / gx, 65535}));
+}
+
 // Rows of a sequence and kv head up to which the row kernel is taken.
 constexpr int kRowKernelRows = 32;
 
@@ -1022,7 +1028,7 @@ template <int D>
 void launch_rows(const AttnArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.max_q * a.group;
   const int64_t gx = (int64_t)a.c.n_kv * a.splits;
-  const dim3 grid((unsigned)gx, (unsigned)std::max<int64_t>(1, std::min<int64_t>(a.c.n_seq, (1 << 22) / gx)));
+  const dim3 grid((unsigned)gx, sequences_at_once(a, gx));
   if (rows <= 8) hipLaunchKernelGGL((attn_rows_kernel<D, 8>), grid, dim3(kThreads), 0, s, a);
   else if (rows <= 16) hipLaunchKernelGGL((attn_rows_kernel<D, 16>), grid, dim3(kThreads), 0, s, a);
   else hipLaunchKernelGGL((attn_rows_kernel<D, 32>), grid, dim3(kThreads), 0, s, a);
@@ -1032,7 +1038,7 @@ template <int D>
 void launch_tiles(const AttnArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.max_q * a.group;
   const int64_t gx = (int64_t)a.c.n_kv * a.splits * ((rows + kTileRows - 1) / kTileRows);
-  const dim3 grid((unsigned)gx, (unsigned)std::max<int64_t>(1, std::min<int64_t>(a.c.n_seq, (1 << 22) / gx)));
+  const dim3 grid((unsigned)gx, sequences_at_once(a, gx));
   hipLaunchKernelGGL((attn_tile_kernel<D>), grid, dim3(kThreads), 0, s, a);
 }
 
