@@ -1044,29 +1044,41 @@ void launch_tiles(const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Parts that a sequence's keys are cut into. A part costs its workgroup about
-// 6 us of start and finish and the join its sums, so parts are made only
-//   - to fill the GPU: up to 512 workgroups, of at least 512 keys each for the
-//     row kernel (one sequence of 333 keys: 13.5 us whole, 18.5 in two) and
-//     256 for the tile kernel, whose workgroups are that much slower (64
-//     positions over 2048 keys: 30 us with 256, 37 with 512); more does not
-//     pay (65536 keys, 8 kv heads: 26.5 us with 512, 32.4 with 1024; 512
-//     positions over 8192 keys: 139 us with 512, 153 with 1024), but for the
-//     tile kernel 768 in two parts of 1024 keys or more are better than 384
-//     (a prompt of 3000 tokens, 16 heads: 108 us against 130; 4 chunks of 128
-//     positions over 4096 keys: 86 against 83);
-//   - for the row kernel, to even out sequences of different lengths: up to
-//     2048 workgroups of at least 1024 keys (32 sequences of 8k to 16k keys:
-//     99.7 us with 2048, 105 with 1024, 117 with 512; 4 sequences: 22.6 us
-//     with 1024 keys each, 25.3 with 512).
+// Parts that a sequence's keys are cut into (times: one layer call in a graph,
+// parts of the given sizes).
+//
+// Row kernel. A wave that has a SIMD to itself takes about 1.05 us for 32 keys
+// (the latency of its loads; 128 keys a workgroup are one step each for its
+// waves), the join 3.6 us. So parts
+//   - of 128 keys or more, while there is a CU for every workgroup (one
+//     sequence of 8 kv heads: 1000 keys 14.1 us whole, 9.8 in 8 parts, 13.1 in
+//     two; 8192 keys 10.8 in 32 parts, 12.8 in 16);
+//   - for two workgroups a CU, if all have 360 keys or more (4 such sequences
+//     of 8192 keys: 16.8 us in 16 parts, 17.6 in 8, 19.4 in 32; 8 of 2500:
+//     13.9 us in 4, 15.1 in 7);
+//   - none where they would not save a wave 448 keys / 4 (16 sequences of 700
+//     keys: 11.5 us whole, 12.7 in two; one of 333 keys: 8.1, 9.6 in four);
+//   - of 1024 keys or more up to 2048 workgroups, to even out sequences of
+//     different lengths (32 sequences of 8k to 16k keys: 99.7 us, 105 with
+//     1024 workgroups, 117 with 512).
+//
+// Tile kernel. Parts of at least 256 keys fill the GPU, up to 512 workgroups
+// (64 positions over 2048 keys: 30 us, 37 with 512 keys; 512 positions over
+// 8192 keys: 139 us, 153 with 1024 workgroups), but 768 in two parts of 1024
+// keys or more are better than 384 (a prompt of 3000 tokens, 16 heads: 108 us
+// against 130; 4 chunks of 128 positions over 4096 keys: 86 against 83).
 int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len) {
   if (n_seq <= 0 || rows <= 0) return 1;
-  const bool few = rows <= kRowKernelRows;
-  const int64_t base = n_seq * n_kv * (few ? 1 : (rows + kTileRows - 1) / kTileRows);
-  const int64_t most = few || base > 384 || max_len < 2048 ? 512 / base : std::max<int64_t>(2, 512 / base);
-  const int64_t fill = std::min((max_len + (few ? 511 : 255)) / (few ? 512 : 256), most);
-  const int64_t even = few ? std::min((max_len + 1023) / 1024, 2048 / base) : 1;
-  return (int)std::max<int64_t>({1, fill, even});
+  if (rows <= kRowKernelRows) {
+    const int64_t base = n_seq * n_kv;
+    int64_t fill = std::max<int64_t>(1, std::min((max_len + 127) / 128, 256 / base));
+    if (max_len >= 360 * (512 / base)) fill = std::max(fill, 512 / base);
+    if (max_len - max_len / fill < 448) fill = 1;
+    return (int)std::max(fill, std::min((max_len + 512) / 1024, 2048 / base));
+  }
+  const int64_t base = n_seq * n_kv * ((rows + kTileRows - 1) / kTileRows);
+  const int64_t most = base > 384 || max_len < 2048 ? 512 / base : std::max<int64_t>(2, 512 / base);
+  return (int)std::max<int64_t>(1, std::min((max_len + 255) / 256, most));
 }
 
 hipError_t launch_kv4_attn(const AttnArgs& a, hipStream_t s) {
