@@ -590,12 +590,22 @@ def _heads(t, name, dev):
     return st if n > 1 else h * d
 
 
-def _new(x, shape, stream, dtype=None):
-    """A tensor on x's device from the pool of the stream that fills it."""
+def _like(x, stream):
+    """A contiguous tensor of x's shape from the pool of the stream that fills it."""
+    torch = _torch()
     if stream is None:
-        return x.new_empty(shape, dtype=dtype)
-    with _torch().cuda.stream(stream):
-        return x.new_empty(shape, dtype=dtype)
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _empty(x, dtype, stream, *shape):
+    """A tensor on x's device, likewise."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=x.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device=x.device)
 
 
 def _flat(t, name, dtype, n, dev):
@@ -647,7 +657,7 @@ def gq_qk_rope(x, pos, rope=None, norm=None, eps: float = 1e-6, out=None, stream
     xs = _heads(x, "x", dev)
     n, h, d = x.shape
     if out is None:
-        out, os_ = _new(x, x.shape, stream), h * d
+        out, os_ = _like(x, stream), h * d
     else:
         os_ = _heads(out, "out", dev)
         if out.shape != x.shape:
@@ -682,7 +692,7 @@ def gq_kv4_append(cache, k, v, lens, q_start=None, rope=None, k_norm=None, q=Non
         if q.shape[0] != n or q.shape[2] != d:
             raise ValueError(f"q must be [{n}, heads, {d}]")
         if q_out is None:
-            q_out, qos = _new(q, q.shape, stream), heads * d
+            q_out, qos = _like(q, stream), heads * d
         else:
             qos = _heads(q_out, "q_out", dev)
             if q_out.shape != q.shape:
@@ -706,14 +716,18 @@ def gq_kv4_read(cache, lens, n_tok: int, q_start=None, K=None, V=None, stream=No
     torch = _torch()
     dev = torch.cuda.current_device()
     starts, lengths = _batch(cache, lens, q_start, n_tok, dev)
-    shape = (n_tok, cache.n_kv, cache.head_dim)
-    if K is None:
-        K = _new(cache.pages, shape, stream, torch.float32)
-    if V is None:
-        V = _new(cache.pages, shape, stream, torch.float32)
     n = n_tok * cache.n_kv * cache.head_dim
-    st = load_library().gq_kv4_read(cache._ref, n_tok, starts, lengths, _flat(K, "K", torch.float32, n, dev),
-                                    _flat(V, "V", torch.float32, n, dev), _stream_handle(stream))
+    if K is None:
+        K = _empty(cache.pages, torch.float32, stream, n_tok, cache.n_kv, cache.head_dim)
+        kp = K.data_ptr()
+    else:
+        kp = _flat(K, "K", torch.float32, n, dev)
+    if V is None:
+        V = _empty(cache.pages, torch.float32, stream, n_tok, cache.n_kv, cache.head_dim)
+        vp = V.data_ptr()
+    else:
+        vp = _flat(V, "V", torch.float32, n, dev)
+    st = load_library().gq_kv4_read(cache._ref, n_tok, starts, lengths, kp, vp, _stream_handle(stream))
     if st != GQ_OK:
         raise GQError(st, "gq_kv4_read")
     return K, V
@@ -744,7 +758,7 @@ def gq_kv4_attn(cache, q, lens, q_start=None, max_q=None, max_len=None, scale=No
     if d != cache.head_dim:
         raise ValueError(f"q must be [tokens, heads, {cache.head_dim}]")
     if out is None:
-        out, os_ = _new(q, q.shape, stream), heads * d
+        out, os_ = _like(q, stream), heads * d
     else:
         os_ = _heads(out, "out", dev)
         if out.shape != q.shape:
@@ -758,7 +772,7 @@ def gq_kv4_attn(cache, q, lens, q_start=None, max_q=None, max_len=None, scale=No
     if need < 0:
         raise GQError(GQ_ERR_SHAPE, "gq_kv4_attn")
     if workspace is None and need > 0:
-        workspace = _new(cache.pages, (need,), stream)
+        workspace = _empty(cache.pages, torch.uint8, stream, need)
     st = lib.gq_kv4_attn(cache._ref, q.data_ptr(), qs, heads, n, starts, lengths, max_q, max_len,
                          d ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(), os_,
                          _flat(workspace, "workspace", torch.uint8, need, dev),
