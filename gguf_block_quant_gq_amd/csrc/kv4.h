@@ -54,6 +54,8 @@ struct AttnArgs {
   int causal;
   int window;   // 0: none
   int splits;   // parts that a sequence's keys are cut into
+  int row_tiles;   // tile kernel: row tiles of every sequence; 0: as many as each has
+  int64_t places;  // tile kernel: row tiles of all sequences
   float* part;  // splits > 1: the parts' sums, and after them their (maximum, total)
 };
 

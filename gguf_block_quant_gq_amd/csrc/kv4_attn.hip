@@ -590,6 +590,42 @@ struct TileCfg {
 
 constexpr int kTileRows = 128;
 
+// The sequence of a place, among the places that ragged sequences have (see
+// launch_tiles), and the first row of its row tile; negative: none. Called by
+// whole waves; the offsets are searched 64 at a time, as in row_position.
+__device__ __forceinline__ int ragged_place(const AttnArgs& a, int64_t place, int* seq, SeqRows* rows) {
+  const Kv4Args& c = a.c;
+  const int lane = threadIdx.x & 63;
+  const auto first_place = [&](int start, int b) {
+    const int64_t row = start < 0 ? 0 : start < c.n_tok ? start : c.n_tok;
+    return row * a.group / kTileRows + b;
+  };
+  int lo = 0, n = c.n_seq;
+  for (;;) {
+    const int step = (n + 63) / 64, i = lo + lane * step;
+    const int b = i < c.n_seq ? i : c.n_seq - 1;
+    const int start = c.q_start[b], end = c.q_start[b + 1], len = c.lens[b];
+    const int64_t p = first_place(start, b);
+    const uint64_t m = __ballot(lane * step < n && p <= place);
+    if (m == 0) return -1;
+    const int at = 63 - __clzll((unsigned long long)m);
+    if (step == 1) {
+      *seq = __builtin_amdgcn_readlane(b, at);
+      const int first = __builtin_amdgcn_readlane(start, at), stop = __builtin_amdgcn_readlane(end, at);
+      const bool ok = first >= 0 && stop >= first && stop <= c.n_tok;
+      rows->first = ok ? first : 0;
+      rows->n = ok ? stop - first : 0;
+      rows->len = __builtin_amdgcn_readlane(len, at);
+      const int64_t its = place - first_place(first, *seq);
+      const int64_t tiles = ((int64_t)(rows->n < a.max_q ? rows->n : a.max_q) * a.group + kTileRows - 1) / kTileRows;
+      return its < tiles ? (int)(tiles - 1 - its) * kTileRows : -1;
+    }
+    const int stop = lo + n;
+    lo += at * step;
+    n = step < stop - lo ? step : stop - lo;
+  }
+}
+
 template <int D>
 __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(AttnArgs a) {
   typedef TileCfg<D> C;
@@ -604,8 +640,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
   // kv heads fastest: neighbours in the grid go to different XCDs, so each
   // XCD's L2 holds few heads. Later rows see more keys and start first.
   const int kvh = blockIdx.x % c.n_kv, rest = blockIdx.x / c.n_kv;
-  const int split = rest % a.splits, row_tiles = gridDim.x / c.n_kv / a.splits;
-  const int row0 = (row_tiles - 1 - rest / a.splits) * kTileRows;
+  const int split = rest % a.splits, slot = rest / a.splits, slots = gridDim.x / (c.n_kv * a.splits);
   const int hd = c.hd, lg = c.page_log2, P = 1 << lg, row_b = hd / 2;
   const int scale_at = kv4_code_bytes(hd, lg), part_b = kv4_part_bytes(hd, lg);
   const int64_t head_at = kv4_part(c, kvh, 0);
@@ -631,11 +666,19 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
   const int vwrite = C::KBYTES + vrow * C::VROW + 2 * sub_key + 16 * (kg & 1) + 8 * (kg >> 1);
   const int kread = m * C::KROW + 16 * h, vread = C::KBYTES + m * C::VROW + 16 * h;
 
-  for (int b = blockIdx.y; b < c.n_seq; b += gridDim.y) {
-    const SeqRows s = seq_rows(c, b);
+  for (int64_t place = slot; place < a.places; place += slots) {
+    int b, row0;
+    SeqRows s;
+    if (a.row_tiles > 0) {
+      b = (int)(place / a.row_tiles);
+      row0 = (a.row_tiles - 1 - (int)(place - (int64_t)b * a.row_tiles)) * kTileRows;
+      s = seq_rows(c, b);
+    } else {
+      row0 = ragged_place(a, place, &b, &s);
+    }
     const int n = s.n < a.max_q ? s.n : a.max_q;
     const int R = n * a.group;
-    if (row0 >= R) continue;
+    if (row0 < 0 || row0 >= R) continue;
     const int len = clamped_len(a, s.len), pos0 = len - s.n;
     const int rlast = (row0 + kTileRows < R ? row0 + kTileRows : R) - 1;
     const Seen first = seen_keys(a, pos0 + row0 / a.group, len), last = seen_keys(a, pos0 + rlast / a.group, len);
@@ -792,29 +835,32 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
       const uint8_t* buf = lds[tile & 1];
       const int key0 = lo + tile * KT;
       // 32 keys at a time, which keeps the scores and weights in 32 registers.
-      // An operand is asked for in LDS one product ahead, the first one of the
-      // values before the softmax (a prompt of 4096 positions, 32 heads: 440 -> 420 us).
+      // Operands are asked for in LDS two products ahead, the first ones of the
+      // values before the softmax (two prompts of about 4096 positions, 32
+      // heads: 440 us without, 420 with one ahead, 417 with two).
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
         if (!wave_on) break;
         f32x16 sc = {};
         __builtin_amdgcn_sched_barrier(0);
         const uint8_t* kb = buf + kread + 32 * k * C::KROW;
-        h8 x = *reinterpret_cast<const h8*>(kb);
+        constexpr int AHEAD = 2;
+        h8 x[AHEAD + 1];
+#pragma unroll
+        for (int w = 0; w < AHEAD; ++w) x[w] = *reinterpret_cast<const h8*>(kb + 32 * w);
 #pragma unroll
         for (int w = 0; w < KS; ++w) {
-          h8 y;
-          if (w + 1 < KS) y = *reinterpret_cast<const h8*>(kb + 32 * (w + 1));
+          if (w + AHEAD < KS) x[(w + AHEAD) % (AHEAD + 1)] = *reinterpret_cast<const h8*>(kb + 32 * (w + AHEAD));
           __builtin_amdgcn_sched_barrier(0);
-          sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, qh[w], sc, 0, 0, 0);
-          sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, ql[w], sc, 0, 0, 0);
-          x = y;
+          sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[w % (AHEAD + 1)], qh[w], sc, 0, 0, 0);
+          sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[w % (AHEAD + 1)], ql[w], sc, 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
         }
         const auto v_at = [&](int u) {
           return *reinterpret_cast<const h8*>(buf + vread + 32 * (u % NT) * C::VROW + 32 * (2 * k + u / NT));
         };
-        x = v_at(0);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) x[u] = v_at(u);
         __builtin_amdgcn_sched_barrier(0);
         if (masked(tile)) {
           // (keys counted from the lane's first one, so that all that differs
@@ -863,13 +909,13 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
+        for (int u = 2; u < AHEAD; ++u) x[u] = v_at(u);
+#pragma unroll
         for (int u = 0; u < 2 * NT; ++u) {
-          h8 y;
-          if (u + 1 < 2 * NT) y = v_at(u + 1);
+          if (u + AHEAD < 2 * NT) x[(u + AHEAD) % (AHEAD + 1)] = v_at(u + AHEAD);
           __builtin_amdgcn_sched_barrier(0);
-          o[u % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, ph[u / NT], o[u % NT], 0, 0, 0);
-          o[u % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, pl[u / NT], o[u % NT], 0, 0, 0);
-          x = y;
+          o[u % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[u % (AHEAD + 1)], ph[u / NT], o[u % NT], 0, 0, 0);
+          o[u % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[u % (AHEAD + 1)], pl[u / NT], o[u % NT], 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -1034,12 +1080,25 @@ void launch_rows(const AttnArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL((attn_rows_kernel<D, 32>), grid, dim3(kThreads), 0, s, a);
 }
 
+// The grid counts places for row tiles. Where sequences have about the same
+// rows, or need no search, each has the row tiles of max_q. Else (fewer places)
+// sequence b has those from floor(q_start[b] group / 128) + b on, as many as
+// its rows can need, one to spare at most; a workgroup finds its sequence by a
+// search for its place. Workgroups without rows cost about 1 us of dispatch
+// each and XCD (64 sequences of one row, one of 2048, 8 kv heads: 366 us with
+// max_q's row tiles for all, 180 by place; 64 of 64 rows with a max_q of 4096:
+// 407, 171). A resident grid that deals places in rounds came out even for two
+// prompts and slower for eight (405 -> 447 us): the dispatcher evens out
+// better.
 template <int D>
-void launch_tiles(const AttnArgs& a, hipStream_t s) {
-  const int64_t rows = (int64_t)a.max_q * a.group;
-  const int64_t gx = (int64_t)a.c.n_kv * a.splits * ((rows + kTileRows - 1) / kTileRows);
-  const dim3 grid((unsigned)gx, sequences_at_once(a, gx));
-  hipLaunchKernelGGL((attn_tile_kernel<D>), grid, dim3(kThreads), 0, s, a);
+void launch_tiles(AttnArgs a, hipStream_t s) {
+  const int64_t tiles = ((int64_t)a.max_q * a.group + kTileRows - 1) / kTileRows;
+  const int64_t ragged = (int64_t)a.c.n_tok * a.group / kTileRows + a.c.n_seq;
+  a.row_tiles = !a.c.q_start || a.c.n_seq * tiles <= ragged ? (int)tiles : 0;
+  a.places = a.row_tiles ? a.c.n_seq * tiles : ragged;
+  const int64_t heads = (int64_t)a.c.n_kv * a.splits;
+  const int64_t slots = std::max<int64_t>(1, std::min(a.places, (1 << 22) / heads));
+  hipLaunchKernelGGL((attn_tile_kernel<D>), dim3((unsigned)(heads * slots)), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace

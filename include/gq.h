@@ -522,8 +522,8 @@ int gq_qk_rope(const float* x, int64_t x_stride, int64_t n_tok, int64_t n_head, 
  * q_start[n_seq] on) are left as they were, and append and read do the same
  * for a row whose position is negative or not below table_stride *
  * page_tokens. Offsets that descend or leave 0 .. n_tok give that sequence no
- * rows. These arrays live on the device
- * and cannot be checked before the launch; whatever they hold, no call reads
+ * rows, and rows of the sequences after it may be left as they were. These
+ * arrays live on the device and cannot be checked before the launch; whatever they hold, no call reads
  * or writes outside the arrays it was given: a page number outside [0,
  * n_pages) is never followed -- nothing is stored through it, reading gives
  * NaN, and attention rows that see a key of it are NaN.

@@ -242,3 +242,48 @@ def test_two_graphs_at_once(gq):
         torch.cuda.synchronize()
         for step, _, _, out, _ in layers:
             assert np.array_equal(to_host(out), to_host(step(None))), turn
+
+
+@pytest.mark.parametrize("n,H,n_kv,hd", [
+    ([1] * 40 + [150, 0, 0, 2] + [1] * 30 + [33, 1], 4, 2, 64),      # more sequences than one search step takes
+    ([0, 128, 0, 32, 33, 1, 0], 8, 2, 128),                          # tiles that end where a sequence does
+    ([31, 1, 64, 95, 1], 4, 1, 256),
+    ([0] * 200 + [40] + [0] * 200, 2, 2, 32),
+])
+def test_prompts_and_single_tokens_in_one_batch(gq, n, H, n_kv, hd):
+    """Row tiles dealt to sequences of very different lengths; rows before the
+    first and behind the last sequence are left as they were."""
+    import torch
+    lens = [m + (17 * i) % 90 for i, m in enumerate(n)]
+    b = Batch(114, n, lens, 16, n_kv, hd)
+    q = queries(b, H)
+    lens, q_start = b.dev()
+    for max_q in (None, max(n)):
+        full = torch.full((b.n_tok + 8, H, hd), 6.0, device="cuda")
+        out = full.clone()
+        full[5:-3] = to_dev(q)
+        gq.gq_kv4_attn(b.cache(gq), full, lens, q_start + 5, max_q=max_q, out=out)
+        got = to_host(out)
+        assert (got[:5] == 6.0).all() and (got[-3:] == 6.0).all()
+        check_attention(b, got[5:-3], q, hd ** -0.5, True, 0)
+
+
+def test_attention_with_offsets_that_are_none(gq):
+    """Offsets that descend or leave the rows: nothing outside the arrays is
+    touched, and sequences before the first such offset are computed (but for
+    rows that a later one claims too)."""
+    import torch
+    b = Batch(115, [40, 3, 100], [40, 3, 100], 32, 2, 96)
+    q = queries(b, 4)
+    cache, dq = b.cache(gq), to_dev(q)
+    lens, q_start = b.dev()
+    want = to_host(gq.gq_kv4_attn(cache, dq, lens, q_start, max_q=100))
+    for bad in ([0, 40, 30, 143], [-5, 40, 43, 143], [0, 40, 43, 999], [2147483647] * 4, [-2147483648] * 4,
+                [0, 2147483647, -2147483648, 143]):
+        guard = torch.full((b.n_tok + 2, 4, 96), 9.0, device="cuda")
+        gq.gq_kv4_attn(cache, dq, lens, to_dev(np.array(bad, np.int32)), max_q=100, out=guard[1:-1])
+        got = to_host(guard)
+        assert (got[0] == 9.0).all() and (got[-1] == 9.0).all()
+        if bad[:2] == [0, 40]:
+            own = min(40, bad[2])
+            assert np.array_equal(got[1:1 + own], want[:own])
