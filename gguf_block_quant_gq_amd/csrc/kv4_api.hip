@@ -1,6 +1,7 @@
 // kv4_api.hip -- the extern "C" entry points of the rotary positions and the
 // paged 4-bit key/value cache (declared in gq.h): argument checks on the
 // host, launch. Every check runs before the first HIP call.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -279,6 +280,9 @@ extern "C" int gq_kv4_attn(const gq_kv4* cache, const float* q, int64_t q_stride
   const int64_t need = attn_ws(cache, n_head, max_q, max_len, &a.splits);
   if (need < 0 || ws_bytes < 0) return GQ_ERR_SHAPE;
   if (n_tok == 0 || a.c.n_seq == 0 || max_q == 0) return GQ_OK;
+  if (window > 0 && window < max_len)  // a sequence's rows see at most this many keys: fewer parts
+    a.splits = std::min(a.splits, gq::kv4_attn_splits(a.c.n_seq, a.c.n_kv, max_q * (n_head / a.c.n_kv),
+                                                      std::min(max_len, window + max_q - 1)));
   if (!q || !out || (need > 0 && !ws)) return GQ_ERR_NULL;
   if (ws_bytes < need) return GQ_ERR_SHAPE;
   if ((st = check_cache_ptrs(a.c)) != GQ_OK) return st;

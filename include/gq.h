@@ -581,7 +581,7 @@ int gq_kv4_read(const gq_kv4* cache, int64_t n_tok, const int32_t* q_start, cons
  * max_q: at least every n_b (rows of a sequence past max_q are left as they
  * were); max_len: at least every lens[b], at most table_stride * page_tokens
  * (a length past max_len is taken as max_len, a negative one as 0).
- * The two and the shapes choose the kernel and how far long sequences are
+ * The two, window and the shapes choose the kernel and how far long sequences are
  * split over workgroups; nothing is read back, so a captured call follows
  * lengths that change between replays, up to max_len. Products take q and
  * the softmax weights as pairs of fp16 numbers on the matrix cores, sums,

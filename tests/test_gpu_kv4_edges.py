@@ -287,3 +287,15 @@ def test_attention_with_offsets_that_are_none(gq):
         if bad[:2] == [0, 40]:
             own = min(40, bad[2])
             assert np.array_equal(got[1:1 + own], want[:own])
+
+
+@pytest.mark.parametrize("n", [[1, 1], [6, 3], [50, 3]])
+@pytest.mark.parametrize("window", [1, 40, 700, 3000, 8999, 9000])
+def test_windows_over_long_sequences(gq, n, window):
+    # cut into the parts that the window's keys call for
+    b = Batch(116, n, [9000, 2500], 64, 1, 64)
+    q = queries(b, 4)
+    lens, q_start = b.dev()
+    for causal in (True, False):
+        out = gq.gq_kv4_attn(b.cache(gq), to_dev(q), lens, q_start, max_q=max(n), causal=causal, window=window)
+        check_attention(b, to_host(out), q, 64 ** -0.5, causal, window)
