@@ -18,7 +18,14 @@
 // value are lane exchanges, and a head may be turned in place (its loads all
 // precede its stores). A workgroup takes a token, or four where there are many:
 // their sines and cosines (about 60 fp64 operations a pair) are computed once
-// into LDS for all heads, with the first heads' loads in flight.
+// into LDS for all heads, with the first heads' loads in flight. Neighbouring
+// lanes read neighbouring 32 bytes, so a wave reads and writes whole kilobytes.
+//
+// Bound: HBM for many tokens. Rotation of 4096 tokens of 32 heads of 128, normed
+// (134 MB): 24.0 us, 5.6 TB/s. Append of 6991 tokens of 32 + 8 + 8 heads (294
+// MB): 67 us, 4.4 TB/s; the blocks' arithmetic (44% of the vector cycles) is not
+// all under the loads. Single tokens: a chain of loads and the angles, 2.5 us
+// for a rotation and 4.8 for an append, of which about 2.2 are the launch.
 #include <algorithm>
 
 #include "gq_device.h"

@@ -151,8 +151,12 @@ __device__ __forceinline__ RowScale row_scale(float largest, float scale) {
 // 15 the lo parts of the same rows, so one product gives both, one lane
 // rotation adds them, and likewise for the weights. ROWS = 32: two column
 // groups (NG) share the dequantised keys and values.
-// Bound: HBM. 144 bytes a token and kv head of 128 channels against about
-// 1500 cycles of issue per 32 keys and SIMD, an issue limit near 7 TB/s.
+// Bound: HBM, nearly. 32 sequences of 8k to 16k keys, 8 kv heads of 128 and 4
+// query heads each (452 MB): 92 us, 4.9 TB/s; its loads alone take 84 us (with
+// cached or nontemporal loads alike), its arithmetic alone 70 (about 1500
+// cycles of issue per 32 keys and SIMD). Three waves a SIMD (128 channels) hide
+// one under the other; four, with fewer registers, took 107 us, a second tile
+// of registers in flight spilled (209). One sequence of 8192 keys: 8.7 us.
 template <int D>
 struct RowTile {
   static constexpr int KW = D / 32;             // dwords of a key per lane
@@ -576,9 +580,15 @@ __global__ __launch_bounds__(kThreads, row_kernel_waves(D, ROWS)) void attn_rows
 //   the lanes l and l ^ 32; the weights go straight into the second product,
 //   whose keys are ordered as the scores lie: chunk 2 t + h of a value row
 //   holds keys 16 t + 4 h + 0 .. 3 and 16 t + 8 + 4 h + 0 .. 3.
-// Bound: issue. Per wave and 64 keys of 128 channels, 128 matrix instructions
-// (about 37 cycles each, which do not overlap vector instructions on this
-// GPU) and about 400 vector ones for softmax and dequantisation.
+// Bound: the matrix cores, and what of the vector work is not under them. Two
+// prompts of 4096 and 2895 positions, 32 / 8 heads of 128: 390 us, 526 TFLOP/s
+// of the formula's operations and twice that with the lo parts. Without softmax
+// and staging the same kernel took 352 us, the rate of a large library product
+// (1170 TFLOP/s; the clock falls to 1.9 GHz under it); the vector work alone
+// takes 275, of which about 40 us stay exposed. The matrix cores and the vector
+// unit work at once only for different waves of a SIMD, hence two workgroups a
+// CU; 256 rows and 8 waves to a workgroup (one barrier for both waves of a
+// SIMD) took 553 us against 464, wave priorities made no difference.
 template <int D>
 struct TileCfg {
   static constexpr int KT = D > 128 ? 32 : 64;      // keys per tile
@@ -971,8 +981,10 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
 // groups of lanes share a row, group g taking parts g, g + GROUPS, ..., and
 // their sums meet in LDS (rows of many parts: a decode step has few rows);
 // else a group has a row to itself (rows of few parts: a prompt chunk has many
-// rows; 32768 rows of two parts took 61 us with a workgroup each). Parts
-// without keys have a maximum of minus infinity and are skipped.
+// rows; 32768 rows of two parts: 13 us, 61 with a workgroup each). Parts
+// without keys have a maximum of minus infinity and are skipped. Bound: the
+// latency of its launch and two dependent loads (32 rows of 32 parts: 3.9 us;
+// 1024 of 16, 8.5 MB: 5.3); HBM for many rows (2048 of 32, 34 MB: 8.9 us).
 template <int LANES, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a) {
   constexpr int GROUPS = kThreads / LANES, STEP = WHOLE ? GROUPS : 1, kAhead = 4;
