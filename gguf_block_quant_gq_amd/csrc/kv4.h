@@ -66,7 +66,7 @@ hipError_t launch_kv4_append(const Kv4Args& c, const HeadArgs& q, const HeadArgs
 hipError_t launch_kv4_read(const Kv4Args& c, float* K, float* V, hipStream_t s);
 // Into how many parts the attention cuts each sequence (1: none, no
 // workspace), and its workspace: the parts' sums and their (maximum, total).
-int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len);
+int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len, int hd);
 hipError_t launch_kv4_attn(const AttnArgs& a, hipStream_t s);
 
 // Where the codes and scales of one kv head's keys (kv = 0) or values (kv =

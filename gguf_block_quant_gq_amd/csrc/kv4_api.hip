@@ -248,7 +248,7 @@ int check_attn_shape(const gq_kv4* cache, int64_t n_head, int64_t max_q, int64_t
 // row and part (none when nothing is split); -1 where 64 bits do not hold it.
 int64_t attn_ws(const gq_kv4* cache, int64_t n_head, int64_t max_q, int64_t max_len, int* splits) {
   const int64_t rows = max_q * (n_head / cache->n_kv);
-  *splits = gq::kv4_attn_splits(cache->n_seq, cache->n_kv, rows, max_len);
+  *splits = gq::kv4_attn_splits(cache->n_seq, cache->n_kv, rows, max_len, (int)cache->head_dim);
   if (*splits <= 1 || cache->n_seq == 0 || rows == 0) return 0;
   const int64_t per = (cache->head_dim + 2) * 4 * *splits;
   if (cache->n_kv * rows > INT64_MAX / per / cache->n_seq) return -1;
@@ -282,7 +282,7 @@ extern "C" int gq_kv4_attn(const gq_kv4* cache, const float* q, int64_t q_stride
   if (n_tok == 0 || a.c.n_seq == 0 || max_q == 0) return GQ_OK;
   if (window > 0 && window < max_len)  // a sequence's rows see at most this many keys: fewer parts
     a.splits = std::min(a.splits, gq::kv4_attn_splits(a.c.n_seq, a.c.n_kv, max_q * (n_head / a.c.n_kv),
-                                                      std::min(max_len, window + max_q - 1)));
+                                                      std::min(max_len, window + max_q - 1), a.c.hd));
   if (!q || !out || (need > 0 && !ws)) return GQ_ERR_NULL;
   if (ws_bytes < need) return GQ_ERR_SHAPE;
   if ((st = check_cache_ptrs(a.c)) != GQ_OK) return st;

@@ -1133,12 +1133,22 @@ void launch_tiles(AttnArgs a, hipStream_t s) {
 //     different lengths (32 sequences of 8k to 16k keys: 99.7 us, 105 with
 //     1024 workgroups, 117 with 512).
 //
-// Tile kernel. Parts of at least 256 keys fill the GPU, up to 512 workgroups
-// (64 positions over 2048 keys: 30 us, 37 with 512 keys; 512 positions over
-// 8192 keys: 139 us, 153 with 1024 workgroups), but 768 in two parts of 1024
-// keys or more are better than 384 (a prompt of 3000 tokens, 16 heads: 108 us
-// against 130; 4 chunks of 128 positions over 4096 keys: 86 against 83).
-int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len) {
+// Tile kernel. A workgroup that has a CU to itself takes 1.1 (64 channels) to
+// 4.4 us (256) for 64 keys. So parts
+//   - of 192 keys or more, while there is a CU for every workgroup (16
+//     positions over 2000 keys, 8 kv heads of 128: 19.7 us in 12 parts, 22.0 in
+//     8; 64 positions over 500 keys: 23.6 us in 3, 26.9 in two);
+//   - of 340 keys or more up to two workgroups a CU, where a CU holds two (512
+//     positions over 8192 keys: 136 us in 4 parts, 159 in two; heads of 256:
+//     170 us in 4 parts, one workgroup a CU, 193 in 8, but 8 sequences of
+//     different lengths 139 us in 8 parts of 1000 keys, 161 in 4);
+//   - none where they would not save a workgroup more than 256 keys (a prompt of
+//     512, 8 kv heads: 28.5 us whole, 31.7 in two);
+//   - two for a few more workgroups than that and 2048 keys or more (a prompt of
+//     3000 tokens, 16 heads: 108 us against 130; 2048 tokens, 4 kv heads of 256:
+//     133 against 158; 1500 tokens 89 against 119; but 512 workgroups of 128
+//     channels: 106 against 90).
+int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len, int hd) {
   if (n_seq <= 0 || rows <= 0) return 1;
   if (rows <= kRowKernelRows) {
     const int64_t base = n_seq * n_kv;
@@ -1148,8 +1158,13 @@ int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len) 
     return (int)std::max(fill, std::min((max_len + 512) / 1024, 2048 / base));
   }
   const int64_t base = n_seq * n_kv * ((rows + kTileRows - 1) / kTileRows);
-  const int64_t most = base > 384 || max_len < 2048 ? 512 / base : std::max<int64_t>(2, 512 / base);
-  return (int)std::max<int64_t>(1, std::min((max_len + 255) / 256, most));
+  int64_t fill = std::max<int64_t>(1, std::min((max_len + 191) / 192, 256 / base));
+  if (hd <= 128) fill = std::max(fill, std::min(max_len / 340, 512 / base));
+  else if (n_seq > 1) fill = std::max(fill, std::min(max_len / 1000, 512 / base));
+  if (max_len - max_len / fill <= 256) fill = 1;
+  if (fill == 1 && max_len >= 2048 && base <= (hd <= 128 ? 384 : 256)) fill = 2;
+  if (fill == 1 && max_len >= 1024 && hd > 128 && base <= 192) fill = 2;
+  return (int)fill;
 }
 
 hipError_t launch_kv4_attn(const AttnArgs& a, hipStream_t s) {
