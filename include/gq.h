@@ -583,7 +583,10 @@ int gq_kv4_read(const gq_kv4* cache, int64_t n_tok, const int32_t* q_start, cons
  * (a length past max_len is taken as max_len, a negative one as 0).
  * The two, window and the shapes choose the kernel and how far long sequences are
  * split over workgroups; nothing is read back, so a captured call follows
- * lengths that change between replays, up to max_len. Products take q and
+ * lengths that change between replays, up to max_len. A batch of prompts and
+ * single tokens is faster as two calls, over the sequences of each kind (their
+ * offsets, lengths and table rows; the other rows are left as they were), each
+ * with its own max_q. Products take q and
  * the softmax weights as pairs of fp16 numbers on the matrix cores, sums,
  * maximum and total are fp32: the error is about that of fp32 arithmetic
  * (2^-22 of each term of the two products). Repeated calls give the same

@@ -299,3 +299,20 @@ def test_windows_over_long_sequences(gq, n, window):
     for causal in (True, False):
         out = gq.gq_kv4_attn(b.cache(gq), to_dev(q), lens, q_start, max_q=max(n), causal=causal, window=window)
         check_attention(b, to_host(out), q, 64 ** -0.5, causal, window)
+
+
+def test_prompts_and_single_tokens_as_two_calls(gq):
+    """The sequences of each kind by slices of the same arrays, into one output."""
+    import torch
+    n = [1] * 6 + [70, 41]
+    b = Batch(117, n, [700, 1, 33, 64, 2000, 90, 100, 300], 16, 2, 128)
+    q = queries(b, 8)
+    lens, q_start = b.dev()
+    whole, dq = b.cache(gq), to_dev(q)
+    out = torch.full(q.shape, 4.0, device="cuda")
+    for lo, hi, max_q in ((0, 6, 1), (6, 8, 70)):
+        cache = gq.KV4Cache(whole.pages, whole.table[lo:hi], 16, 2, 128)
+        gq.gq_kv4_attn(cache, dq, lens[lo:hi], q_start[lo:hi + 1], max_q=max_q, out=out)
+        if lo == 0:
+            assert (to_host(out)[6:] == 4.0).all()
+    check_attention(b, to_host(out), q, 128 ** -0.5, True, 0)
