@@ -16,14 +16,16 @@
 // Split. hd / 8 lanes (rounded up to a power of two) own a head, 8 channels
 // each; a wave holds whole heads, so the norm's sum and the block's largest
 // value are lane exchanges, and a head may be turned in place (its loads all
-// precede its stores). A workgroup takes a token, or four where there are many:
-// their sines and cosines (about 60 fp64 operations a pair) are computed once
-// into LDS for all heads, with the first heads' loads in flight. Neighbouring
-// lanes read neighbouring 32 bytes, so a wave reads and writes whole kilobytes.
+// precede its stores). A workgroup takes a token, or two where there are many
+// (four: 1500 tokens with half pairs 24 us instead of 19, 4096 + 2895 83 instead
+// of 79; the registers leave fewer waves): their sines and cosines (about 60
+// fp64 operations a pair) are computed once into LDS for all heads, with the
+// first heads' loads in flight. Neighbouring lanes read neighbouring 32 bytes,
+// so a wave reads and writes whole kilobytes.
 //
 // Bound: HBM for many tokens. Rotation of 4096 tokens of 32 heads of 128, normed
-// (134 MB): 24.0 us, 5.6 TB/s. Append of 6991 tokens of 32 + 8 + 8 heads (294
-// MB): 67 us, 4.4 TB/s; the blocks' arithmetic (44% of the vector cycles) is not
+// (134 MB): 23.5 us, 5.7 TB/s. Append of 6991 tokens of 32 + 8 + 8 heads (294
+// MB): 67 us, 4.4 TB/s; the blocks' arithmetic (47% of the vector cycles) is not
 // all under the loads. Single tokens: a chain of loads and the angles, 2.5 us
 // for a rotation and 4.8 for an append, of which about 2.2 are the launch.
 #include <algorithm>
@@ -405,7 +407,7 @@ constexpr int kManyRows = 1024;
 template <int GL, bool APPEND, bool APART, bool FAST>
 void launch_qk_as(const QkArgs& a, int heads, hipStream_t s) {
   if (a.n_tok >= kManyRows) {
-    constexpr int TOK = 4;
+    constexpr int TOK = 2;
     const int gx = std::min((a.n_tok + TOK - 1) / TOK, 1 << 20);
     hipLaunchKernelGGL((qk_rope_kernel<GL, TOK, APPEND, APART, FAST>), dim3(gx), dim3(kThreads), 0, s, a);
   } else {
