@@ -316,3 +316,23 @@ def test_prompts_and_single_tokens_as_two_calls(gq):
         if lo == 0:
             assert (to_host(out)[6:] == 4.0).all()
     check_attention(b, to_host(out), q, 128 ** -0.5, True, 0)
+
+
+@pytest.mark.parametrize("n,lens,H,n_kv,hd", [
+    ([2100], [2100], 2, 1, 64),
+    ([2100, 33], [2100, 1500], 4, 2, 128),
+    ([1, 1, 1, 1, 1], [9000, 0, 576, 577, 1], 4, 2, 64),
+    ([5, 8, 3], [9000, 20, 700], 4, 1, 256),
+])
+def test_lengths_far_under_the_bound(gq, n, lens, H, n_kv, hd):
+    """Parts without keys: sequences and rows with few keys under a bound that
+    others reach, and under one far above every length."""
+    b = Batch(118, n, lens, 64, n_kv, hd)
+    b.table = np.concatenate((b.table, np.full((len(n), 600), -1, np.int32)), 1)
+    q = queries(b, H)
+    dev_lens, q_start = b.dev()
+    rows = None if b.n_tok < 20 else [0, 1, 31, 32, 255, 256, 383, 384, 576, 577, 1000, 2047, 2099] + list(range(2100, b.n_tok))
+    for max_len in (max(lens), b.table.shape[1] * 64):
+        for causal in (True, False):
+            out = gq.gq_kv4_attn(b.cache(gq), to_dev(q), dev_lens, q_start, max_q=max(n), max_len=max_len, causal=causal)
+            check_attention(b, to_host(out), q, hd ** -0.5, causal, 0, rows=rows)
