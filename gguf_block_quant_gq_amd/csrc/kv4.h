@@ -56,6 +56,7 @@ struct AttnArgs {
   int splits;   // parts that a sequence's keys are cut into
   int row_tiles;   // tile kernel: row tiles of every sequence; 0: as many as each has
   int64_t places;  // tile kernel: row tiles of all sequences
+  int64_t first;   // this launch's first sequence (row kernel) or place
   float* part;  // splits > 1: the parts' sums, and after them their (maximum, total)
 };
 

@@ -213,355 +213,353 @@ __global__ __launch_bounds__(kThreads, row_kernel_waves(D, ROWS)) void attn_rows
   const int64_t head_at = kv4_part(c, kvh, 0);
   const int part_b = kv4_part_bytes(hd, lg);
 
-  for (int b = blockIdx.y; b < c.n_seq; b += gridDim.y) {
-    const SeqRows s = seq_rows(c, b);
-    const int n = s.n < a.max_q ? s.n : a.max_q;
-    const int R = n * a.group;
-    if (n <= 0) continue;
-    const int len = clamped_len(a, s.len);
-    // the first and last rows' keys bound everyone's
-    const int pos0 = len - s.n;
-    const Seen first = seen_keys(a, pos0, len), last = seen_keys(a, pos0 + n - 1, len);
-    Seen mine[NG];
+  const int b = (int)a.first + blockIdx.y;
+  const SeqRows s = seq_rows(c, b);
+  const int n = s.n < a.max_q ? s.n : a.max_q;
+  const int R = n * a.group;
+  if (n <= 0) return;
+  const int len = clamped_len(a, s.len);
+  // the first and last rows' keys bound everyone's
+  const int pos0 = len - s.n;
+  const Seen first = seen_keys(a, pos0, len), last = seen_keys(a, pos0 + n - 1, len);
+  Seen mine[NG];
 #pragma unroll
-    for (int q = 0; q < NG; ++q) mine[q] = seen_keys(a, pos0 + (row + 16 * q) / a.group, len);
-    const int lo = first.lo & ~(kTile - 1), hi = last.hi;
-    const int tiles = hi > first.lo ? (hi - lo + kTile - 1) / kTile : 0;
-    const int parts = a.splits * kWaves, mypart = split * kWaves + wave;
-    const int each = (int)((unsigned)tiles / (unsigned)parts), more = tiles - each * parts;
-    const int tile0 = mypart * each + (mypart < more ? mypart : more), tile1 = tile0 + each + (mypart < more ? 1 : 0);
-    const int begin = lo + tile0 * kTile, end = lo + tile1 * kTile;
+  for (int q = 0; q < NG; ++q) mine[q] = seen_keys(a, pos0 + (row + 16 * q) / a.group, len);
+  const int lo = first.lo & ~(kTile - 1), hi = last.hi;
+  const int tiles = hi > first.lo ? (hi - lo + kTile - 1) / kTile : 0;
+  const int parts = a.splits * kWaves, mypart = split * kWaves + wave;
+  const int each = (int)((unsigned)tiles / (unsigned)parts), more = tiles - each * parts;
+  const int tile0 = mypart * each + (mypart < more ? mypart : more), tile1 = tile0 + each + (mypart < more ? 1 : 0);
+  const int begin = lo + tile0 * kTile, end = lo + tile1 * kTile;
 
-    // the query operand: lane (m, g) holds the channels that its key lanes
-    // hold, of row m (FUSED: the hi part of row m, or the lo part of row m - 8);
-    // loaded first, and made operands with the first tile's loads in flight
-    f32x4 qx[NG][KW][2];
+  // the query operand: lane (m, g) holds the channels that its key lanes
+  // hold, of row m (FUSED: the hi part of row m, or the lo part of row m - 8);
+  // loaded first, and made operands with the first tile's loads in flight
+  f32x4 qx[NG][KW][2];
 #pragma unroll
-    for (int q = 0; q < NG; ++q) {
-      const int r = row + 16 * q < R ? row + 16 * q : 0;
-      const float* qr = a.q + (int64_t)(s.first + r / a.group) * a.q_stride + (int64_t)(kvh * a.group + r % a.group) * hd;
+  for (int q = 0; q < NG; ++q) {
+    const int r = row + 16 * q < R ? row + 16 * q : 0;
+    const float* qr = a.q + (int64_t)(s.first + r / a.group) * a.q_stride + (int64_t)(kvh * a.group + r % a.group) * hd;
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const int c0 = (g * KW + w) * 8, at = c0 < hd ? c0 : 0;
-        qx[q][w][0] = load_f32x4(qr + at), qx[q][w][1] = load_f32x4(qr + at + 4);
-      }
+    for (int w = 0; w < KW; ++w) {
+      const int c0 = (g * KW + w) * 8, at = c0 < hd ? c0 : 0;
+      qx[q][w][0] = load_f32x4(qr + at), qx[q][w][1] = load_f32x4(qr + at + 4);
     }
+  }
 
-    const int32_t* table = c.table + (int64_t)b * c.table_stride;
-    const auto page_id = [&](int key) { return table[(key < hi ? key : hi - 1) >> lg]; };
-    // a page number that is none: nothing is read, and the scores are NaN
-    const auto page_ok = [&](int id) { return id >= 0 && id < c.n_pages; };
-    const auto page_buffer = [&](int id) {
-      const bool ok = page_ok(id);
-      return __builtin_amdgcn_make_buffer_rsrc(c.pages + (int64_t)(ok ? id : 0) * c.page_bytes + head_at, 0,
-                                               ok ? 2 * part_b : 0, kBufferFlags);
-    };
-    Tile x;
-    const auto load_keys = [&](int key0, int id0, int id1) {
+  const int32_t* table = c.table + (int64_t)b * c.table_stride;
+  const auto page_id = [&](int key) { return table[(key < hi ? key : hi - 1) >> lg]; };
+  // a page number that is none: nothing is read, and the scores are NaN
+  const auto page_ok = [&](int id) { return id >= 0 && id < c.n_pages; };
+  const auto page_buffer = [&](int id) {
+    const bool ok = page_ok(id);
+    return __builtin_amdgcn_make_buffer_rsrc(c.pages + (int64_t)(ok ? id : 0) * c.page_bytes + head_at, 0,
+                                             ok ? 2 * part_b : 0, kBufferFlags);
+  };
+  Tile x;
+  const auto load_keys = [&](int key0, int id0, int id1) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int id = u ? id1 : id0, slot0 = (key0 + 16 * u) & (P - 1);
-        const __amdgpu_buffer_rsrc_t rs = page_buffer(id);
-        if constexpr (KW == 2) {
-          const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, koff, slot0 * row_b, 0));
-          x.k[u][0] = v.x, x.k[u][1] = v.y;
+    for (int u = 0; u < 2; ++u) {
+      const int id = u ? id1 : id0, slot0 = (key0 + 16 * u) & (P - 1);
+      const __amdgpu_buffer_rsrc_t rs = page_buffer(id);
+      if constexpr (KW == 2) {
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, koff, slot0 * row_b, 0));
+        x.k[u][0] = v.x, x.k[u][1] = v.y;
+      } else {
+#pragma unroll
+        for (int w = 0; w < KW; w += 4) {
+          const u32x4 v =
+              __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, koff + 4 * w, slot0 * row_b, 0));
+          x.k[u][w] = v.x, x.k[u][w + 1] = v.y, x.k[u][w + 2] = v.z, x.k[u][w + 3] = v.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < Tile::KS; ++i)
+        x.ks[u][i] = __builtin_amdgcn_raw_buffer_load_b16(rs, ksoff[i], scale_at + 2 * slot0, 0);
+    }
+  };
+  const auto load_values = [&](int key0, int id0, int id1) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int id = u ? id1 : id0, slot0 = (key0 + 16 * u) & (P - 1);
+      const __amdgpu_buffer_rsrc_t rs = page_buffer(id);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (D == 64) {
+          x.v[4 * u + j][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, voff[j], part_b + slot0 * row_b, 0);
+        } else if constexpr (D == 128) {
+          x.v[4 * u + j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, voff[j], part_b + slot0 * row_b, 0);
         } else {
-#pragma unroll
-          for (int w = 0; w < KW; w += 4) {
-            const u32x4 v =
-                __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, koff + 4 * w, slot0 * row_b, 0));
-            x.k[u][w] = v.x, x.k[u][w + 1] = v.y, x.k[u][w + 2] = v.z, x.k[u][w + 3] = v.w;
-          }
+          const u32x2 v = __builtin_bit_cast(
+              u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, voff[j], part_b + slot0 * row_b, 0));
+          x.v[4 * u + j][0] = v.x, x.v[4 * u + j][1] = v.y;
         }
-#pragma unroll
-        for (int i = 0; i < Tile::KS; ++i)
-          x.ks[u][i] = __builtin_amdgcn_raw_buffer_load_b16(rs, ksoff[i], scale_at + 2 * slot0, 0);
       }
-    };
-    const auto load_values = [&](int key0, int id0, int id1) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int id = u ? id1 : id0, slot0 = (key0 + 16 * u) & (P - 1);
-        const __amdgpu_buffer_rsrc_t rs = page_buffer(id);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (D == 64) {
-            x.v[4 * u + j][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, voff[j], part_b + slot0 * row_b, 0);
-          } else if constexpr (D == 128) {
-            x.v[4 * u + j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, voff[j], part_b + slot0 * row_b, 0);
-          } else {
-            const u32x2 v = __builtin_bit_cast(
-                u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, voff[j], part_b + slot0 * row_b, 0));
-            x.v[4 * u + j][0] = v.x, x.v[4 * u + j][1] = v.y;
-          }
-        }
-        x.vs[u] = __builtin_bit_cast(
-            u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, vsoff, part_b + scale_at + 2 * slot0, 0));
-      }
-    };
-
-    int id0 = 0, id1 = 0;
-    if (begin < end) {
-      id0 = page_id(begin), id1 = page_id(begin + 16);
-      load_keys(begin, id0, id1);
-      load_values(begin, id0, id1);
+      x.vs[u] = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, vsoff, part_b + scale_at + 2 * slot0, 0));
     }
+  };
 
-    h8 qh[NG][KW], ql[NG][FUSED ? 1 : KW];
-    float down[NG];
+  int id0 = 0, id1 = 0;
+  if (begin < end) {
+    id0 = page_id(begin), id1 = page_id(begin + 16);
+    load_keys(begin, id0, id1);
+    load_values(begin, id0, id1);
+  }
+
+  h8 qh[NG][KW], ql[NG][FUSED ? 1 : KW];
+  float down[NG];
 #pragma unroll
-    for (int q = 0; q < NG; ++q) {
-      float big = 0.f;
+  for (int q = 0; q < NG; ++q) {
+    float big = 0.f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      const bool in = row + 16 * q < R && (g * KW + w) * 8 < hd;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float y = in ? qx[q][w][i >> 2][i & 3] : 0.f;
+        qx[q][w][i >> 2][i & 3] = y;
+        big = fmaxf(big, __builtin_fabsf(y));
+      }
+    }
+    const RowScale rs = row_scale(max_over_rows(big), a.scale);
+    down[q] = rs.down;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) {
+      h8 h, l;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e = slot_channel(j);
+        const float y = qx[q][w][e >> 2][e & 3] * rs.up;
+        h[j] = (_Float16)y;
+        l[j] = (_Float16)(y - (float)h[j]);
+      }
+      if constexpr (FUSED) {
+        qh[q][w] = m < 8 ? h : l;
+      } else {
+        qh[q][w] = h;
+        ql[q][w] = l;
+      }
+    }
+  }
+
+  f32x4 o[NG][NT];
+  float mx[NG], l[NG];
+#pragma unroll
+  for (int q = 0; q < NG; ++q) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[q][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    mx[q] = -INFINITY, l[q] = 0.f;
+  }
+
+  // Keys and values have one set of registers each: the next tile's keys are
+  // requested when this tile's have been multiplied, its values likewise, and
+  // page numbers a tile before that. The loads past the last tile repeat it:
+  // were they skipped, the waits would have to be for all loads in flight.
+  // (The scheduling barriers keep the parts of a tile apart, whose operands
+  // would otherwise be live at once.)
+  for (int key0 = begin; key0 < end; key0 += kTile) {
+    const int next = key0 + kTile < end ? key0 + kTile : key0;
+    const int jd0 = page_id(next), jd1 = page_id(next + 16);
+    // scores: rows are this half tile's keys 4 g + r, columns query rows
+    f32x4 sc[NG][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int q = 0; q < NG; ++q) sc[q][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const uint32_t none = page_ok(u ? id1 : id0) ? 0u : 0x7E00u;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        const bool in = row + 16 * q < R && (g * KW + w) * 8 < hd;
+        const h2 d = both(x.ks[u][w / 4] | none);
+        const h8 k = key_operand(x.k[u][w], d, minus8(d));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float y = in ? qx[q][w][i >> 2][i & 3] : 0.f;
-          qx[q][w][i >> 2][i & 3] = y;
-          big = fmaxf(big, __builtin_fabsf(y));
-        }
-      }
-      const RowScale rs = row_scale(max_over_rows(big), a.scale);
-      down[q] = rs.down;
-#pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        h8 h, l;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = slot_channel(j);
-          const float y = qx[q][w][e >> 2][e & 3] * rs.up;
-          h[j] = (_Float16)y;
-          l[j] = (_Float16)(y - (float)h[j]);
-        }
-        if constexpr (FUSED) {
-          qh[q][w] = m < 8 ? h : l;
-        } else {
-          qh[q][w] = h;
-          ql[q][w] = l;
+        for (int q = 0; q < NG; ++q) {
+          sc[q][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[q][w], sc[q][u], 0, 0, 0);
+          if constexpr (!FUSED) sc[q][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[q][w], sc[q][u], 0, 0, 0);
         }
       }
     }
-
-    f32x4 o[NG][NT];
-    float mx[NG], l[NG];
+    __builtin_amdgcn_sched_barrier(0);
+    load_keys(next, jd0, jd1);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (FUSED) {
 #pragma unroll
-    for (int q = 0; q < NG; ++q) {
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) o[q][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      mx[q] = -INFINITY, l[q] = 0.f;
+        for (int r = 0; r < 4; ++r) sc[0][u][r] += dpp_f32<0x128>(sc[0][u][r]);  // row_ror:8: hi + lo
     }
-
-    // Keys and values have one set of registers each: the next tile's keys are
-    // requested when this tile's have been multiplied, its values likewise, and
-    // page numbers a tile before that. The loads past the last tile repeat it:
-    // were they skipped, the waits would have to be for all loads in flight.
-    // (The scheduling barriers keep the parts of a tile apart, whose operands
-    // would otherwise be live at once.)
-    for (int key0 = begin; key0 < end; key0 += kTile) {
-      const int next = key0 + kTile < end ? key0 + kTile : key0;
-      const int jd0 = page_id(next), jd1 = page_id(next + 16);
-      // scores: rows are this half tile's keys 4 g + r, columns query rows
-      f32x4 sc[NG][2];
+    // masks, in tiles that reach past some row's keys. There a value whose
+    // scale is not finite must not meet the zero weight of a row that does
+    // not see it: it is taken as 0, and its key's scores as NaN for the
+    // rows that do. Elsewhere it reaches every row by itself.
+    if (key0 + kTile > first.hi || key0 < last.lo) {
+      uint32_t bad = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int q = 0; q < NG; ++q) sc[q][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const uint32_t none = page_ok(u ? id1 : id0) ? 0u : 0x7E00u;
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t bits = (x.vs[u][r >> 1] >> (16 * (r & 1))) & 0xFFFF;
+          const bool out = key0 + 16 * u + 4 * g + r >= hi;
+          const bool inf = (bits & 0x7C00) == 0x7C00;
+          const uint64_t any = __ballot(inf && !out);
+          if ((any >> (16 * g)) & 0xFFFF) bad |= 1u << (4 * u + r);
+          if (inf || out) x.vs[u][r >> 1] &= r & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+        }
+      }
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          const h2 d = both(x.ks[u][w / 4] | none);
-          const h8 k = key_operand(x.k[u][w], d, minus8(d));
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int key = key0 + 16 * u + 4 * g + r;
 #pragma unroll
           for (int q = 0; q < NG; ++q) {
-            sc[q][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, qh[q][w], sc[q][u], 0, 0, 0);
-            if constexpr (!FUSED) sc[q][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[q][w], sc[q][u], 0, 0, 0);
+            if (bad >> (4 * u + r) & 1) sc[q][u][r] = __builtin_nanf("");
+            if (key < mine[q].lo || key >= mine[q].hi) sc[q][u][r] = -INFINITY;
           }
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
-      load_keys(next, jd0, jd1);
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (FUSED) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) sc[0][u][r] += dpp_f32<0x128>(sc[0][u][r]);  // row_ror:8: hi + lo
-      }
-      // masks, in tiles that reach past some row's keys. There a value whose
-      // scale is not finite must not meet the zero weight of a row that does
-      // not see it: it is taken as 0, and its key's scores as NaN for the
-      // rows that do. Elsewhere it reaches every row by itself.
-      if (key0 + kTile > first.hi || key0 < last.lo) {
-        uint32_t bad = 0;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const uint32_t bits = (x.vs[u][r >> 1] >> (16 * (r & 1))) & 0xFFFF;
-            const bool out = key0 + 16 * u + 4 * g + r >= hi;
-            const bool inf = (bits & 0x7C00) == 0x7C00;
-            const uint64_t any = __ballot(inf && !out);
-            if ((any >> (16 * g)) & 0xFFFF) bad |= 1u << (4 * u + r);
-            if (inf || out) x.vs[u][r >> 1] &= r & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int key = key0 + 16 * u + 4 * g + r;
-#pragma unroll
-            for (int q = 0; q < NG; ++q) {
-              if (bad >> (4 * u + r) & 1) sc[q][u][r] = __builtin_nanf("");
-              if (key < mine[q].lo || key >= mine[q].hi) sc[q][u][r] = -INFINITY;
-            }
-          }
-        }
-      }
-      h8 wl[NG], wh[NG];
-#pragma unroll
-      for (int q = 0; q < NG; ++q) {
-        float top = fmaxf(fmaxf(fmaxf(sc[q][0][0], sc[q][0][1]), fmaxf(sc[q][0][2], sc[q][0][3])),
-                          fmaxf(fmaxf(sc[q][1][0], sc[q][1][1]), fmaxf(sc[q][1][2], sc[q][1][3])));
-        top = max_over_rows(top) * down[q];
-        if (__any(top > mx[q] + kSlack)) {
-          const float nm = fmaxf(mx[q], top);
-          const float f = __builtin_amdgcn_exp2f(mx[q] - (nm == -INFINITY ? 0.f : nm));
-          mx[q] = nm;
-          l[q] *= f;
-#pragma unroll
-          for (int i = 0; i < NT; ++i) o[q][i] *= f;
-        }
-        const float base = mx[q] == -INFINITY ? 0.f : mx[q];
-        const float part = FUSED && m < 8 ? 0.f : -1.f;
-        h2 ph[4], pl[4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-          for (int r = 0; r < 4; r += 2) {
-            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][u][r], down[q], -base));
-            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][u][r + 1], down[q], -base));
-            l[q] += p0 + p1;
-            // (FUSED: p itself in the hi columns)
-            ph[2 * u + r / 2] = hi_parts(p0, p1);
-            pl[2 * u + r / 2] = lo_parts(ph[2 * u + r / 2], p0, p1, part);
-          }
-        }
-        wl[q] = as_h8(pl[0], pl[1], pl[2], pl[3]);
-        wh[q] = as_h8(ph[0], ph[1], ph[2], ph[3]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      // values: pairs of keys side by side, channel by channel
-      h2 vd[4], voffs[4];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        vd[p] = __builtin_bit_cast(h2, (uint32_t)x.vs[p >> 1][p & 1]);
-        voffs[p] = minus8(vd[p]);
-      }
-#pragma unroll
-      for (int w = 0; w < VW; ++w) {
-#pragma unroll
-        for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
-          __builtin_amdgcn_sched_barrier(0);
-          // bytes (2 half) and (2 half + 1) of the pairs' dwords, interleaved
-          uint32_t lo4[4], hi4[4];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint32_t y = __builtin_amdgcn_perm(x.v[2 * p + 1][w], x.v[2 * p][w], half ? 0x07030602u : 0x05010400u);
-            lo4[p] = y & 0x0F0F0F0Fu;
-            hi4[p] = (y >> 4) & 0x0F0F0F0Fu;
-          }
-          // D = 64: the lane's channels are every second one; else even
-          // channels lie in the low half of a dword, odd ones in the high
-          const auto tile = [&](int i, h8 v) {
-            const int at = D == 64 ? i : w * 8 + 2 * i + half;
-#pragma unroll
-            for (int q = 0; q < NG; ++q) {
-              o[q][at] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, wl[q], o[q][at], 0, 0, 0);
-              if constexpr (!FUSED) o[q][at] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, wh[q], o[q][at], 0, 0, 0);
-            }
-          };
-          tile(0, as_h8(two_values<0>(lo4[0], vd[0], voffs[0]), two_values<0>(lo4[1], vd[1], voffs[1]),
-                        two_values<0>(lo4[2], vd[2], voffs[2]), two_values<0>(lo4[3], vd[3], voffs[3])));
-          tile(1, as_h8(two_values<0>(hi4[0], vd[0], voffs[0]), two_values<0>(hi4[1], vd[1], voffs[1]),
-                        two_values<0>(hi4[2], vd[2], voffs[2]), two_values<0>(hi4[3], vd[3], voffs[3])));
-          tile(2, as_h8(two_values<1>(lo4[0], vd[0], voffs[0]), two_values<1>(lo4[1], vd[1], voffs[1]),
-                        two_values<1>(lo4[2], vd[2], voffs[2]), two_values<1>(lo4[3], vd[3], voffs[3])));
-          tile(3, as_h8(two_values<1>(hi4[0], vd[0], voffs[0]), two_values<1>(hi4[1], vd[1], voffs[1]),
-                        two_values<1>(hi4[2], vd[2], voffs[2]), two_values<1>(hi4[3], vd[3], voffs[3])));
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      id0 = jd0, id1 = jd1;
-      load_values(next, id0, id1);
     }
-
-    // the waves' sums, in wave order
+    h8 wl[NG], wh[NG];
 #pragma unroll
     for (int q = 0; q < NG; ++q) {
-      l[q] = sum_over_rows(l[q]);
-      if (g == 0) sm[wave][16 * q + m] = mx[q], sl[wave][16 * q + m] = l[q];
+      float top = fmaxf(fmaxf(fmaxf(sc[q][0][0], sc[q][0][1]), fmaxf(sc[q][0][2], sc[q][0][3])),
+                        fmaxf(fmaxf(sc[q][1][0], sc[q][1][1]), fmaxf(sc[q][1][2], sc[q][1][3])));
+      top = max_over_rows(top) * down[q];
+      if (__any(top > mx[q] + kSlack)) {
+        const float nm = fmaxf(mx[q], top);
+        const float f = __builtin_amdgcn_exp2f(mx[q] - (nm == -INFINITY ? 0.f : nm));
+        mx[q] = nm;
+        l[q] *= f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) o[q][i] *= f;
+      }
+      const float base = mx[q] == -INFINITY ? 0.f : mx[q];
+      const float part = FUSED && m < 8 ? 0.f : -1.f;
+      h2 ph[4], pl[4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+          const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][u][r], down[q], -base));
+          const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][u][r + 1], down[q], -base));
+          l[q] += p0 + p1;
+          // (FUSED: p itself in the hi columns)
+          ph[2 * u + r / 2] = hi_parts(p0, p1);
+          pl[2 * u + r / 2] = lo_parts(ph[2 * u + r / 2], p0, p1, part);
+        }
+      }
+      wl[q] = as_h8(pl[0], pl[1], pl[2], pl[3]);
+      wh[q] = as_h8(ph[0], ph[1], ph[2], ph[3]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    // values: pairs of keys side by side, channel by channel
+    h2 vd[4], voffs[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      vd[p] = __builtin_bit_cast(h2, (uint32_t)x.vs[p >> 1][p & 1]);
+      voffs[p] = minus8(vd[p]);
+    }
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+#pragma unroll
+      for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
+        __builtin_amdgcn_sched_barrier(0);
+        // bytes (2 half) and (2 half + 1) of the pairs' dwords, interleaved
+        uint32_t lo4[4], hi4[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t y = __builtin_amdgcn_perm(x.v[2 * p + 1][w], x.v[2 * p][w], half ? 0x07030602u : 0x05010400u);
+          lo4[p] = y & 0x0F0F0F0Fu;
+          hi4[p] = (y >> 4) & 0x0F0F0F0Fu;
+        }
+        // D = 64: the lane's channels are every second one; else even
+        // channels lie in the low half of a dword, odd ones in the high
+        const auto tile = [&](int i, h8 v) {
+          const int at = D == 64 ? i : w * 8 + 2 * i + half;
+#pragma unroll
+          for (int q = 0; q < NG; ++q) {
+            o[q][at] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, wl[q], o[q][at], 0, 0, 0);
+            if constexpr (!FUSED) o[q][at] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, wh[q], o[q][at], 0, 0, 0);
+          }
+        };
+        tile(0, as_h8(two_values<0>(lo4[0], vd[0], voffs[0]), two_values<0>(lo4[1], vd[1], voffs[1]),
+                      two_values<0>(lo4[2], vd[2], voffs[2]), two_values<0>(lo4[3], vd[3], voffs[3])));
+        tile(1, as_h8(two_values<0>(hi4[0], vd[0], voffs[0]), two_values<0>(hi4[1], vd[1], voffs[1]),
+                      two_values<0>(hi4[2], vd[2], voffs[2]), two_values<0>(hi4[3], vd[3], voffs[3])));
+        tile(2, as_h8(two_values<1>(lo4[0], vd[0], voffs[0]), two_values<1>(lo4[1], vd[1], voffs[1]),
+                      two_values<1>(lo4[2], vd[2], voffs[2]), two_values<1>(lo4[3], vd[3], voffs[3])));
+        tile(3, as_h8(two_values<1>(hi4[0], vd[0], voffs[0]), two_values<1>(hi4[1], vd[1], voffs[1]),
+                      two_values<1>(hi4[2], vd[2], voffs[2]), two_values<1>(hi4[3], vd[3], voffs[3])));
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    id0 = jd0, id1 = jd1;
+    load_values(next, id0, id1);
+  }
+
+  // the waves' sums, in wave order
+#pragma unroll
+  for (int q = 0; q < NG; ++q) {
+    l[q] = sum_over_rows(l[q]);
+    if (g == 0) sm[wave][16 * q + m] = mx[q], sl[wave][16 * q + m] = l[q];
+  }
+  __syncthreads();
+  float f[NG];
+#pragma unroll
+  for (int q = 0; q < NG; ++q) {
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm[w][16 * q + m]);
+    f[q] = __builtin_amdgcn_exp2f(mx[q] - (M == -INFINITY ? 0.f : M));
+  }
+  const int64_t slot0 = (((int64_t)b * c.n_kv + kvh) * a.splits + split) * ((int64_t)a.max_q * a.group);
+  float* ml = a.part + (int64_t)c.n_seq * c.n_kv * a.splits * a.max_q * a.group * hd;
+  for (int p = 0; p < PASS; ++p) {
+    if (p) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (i / TP == p) {
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+          f32x4 v = o[q][i];
+          if constexpr (FUSED) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] += dpp_f32<0x128>(v[r]);
+          }
+          v *= f[q];
+          if (!FUSED || m < 8) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) so[wave][row + 16 * q][(4 * g + r) * TP + i % TP] = v[r];
+          }
+        }
+      }
     }
     __syncthreads();
-    float f[NG];
+    for (int e = threadIdx.x; e < R * TP * 16; e += kThreads) {
+      const int r = e / (TP * 16), q = e % (TP * 16);
+      // place q: lane row q / TP, tile p TP + q % TP
+      const int qm = q / TP, i = p * TP + q % TP;
+      const int ch = D == 64 ? 8 * (qm >> 1) + (qm & 1) + 2 * i : qm * NT + i;
+      if (ch >= hd) continue;
+      float RM = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < NG; ++q) {
-      float M = -INFINITY;
+      for (int w = 0; w < kWaves; ++w) RM = fmaxf(RM, sm[w][r]);
+      const float rb = RM == -INFINITY ? 0.f : RM;
+      float sum = 0.f, tot = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) M = fmaxf(M, sm[w][16 * q + m]);
-      f[q] = __builtin_amdgcn_exp2f(mx[q] - (M == -INFINITY ? 0.f : M));
-    }
-    const int64_t slot0 = (((int64_t)b * c.n_kv + kvh) * a.splits + split) * ((int64_t)a.max_q * a.group);
-    float* ml = a.part + (int64_t)c.n_seq * c.n_kv * a.splits * a.max_q * a.group * hd;
-    for (int p = 0; p < PASS; ++p) {
-      if (p) __syncthreads();
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        if (i / TP == p) {
-#pragma unroll
-          for (int q = 0; q < NG; ++q) {
-            f32x4 v = o[q][i];
-            if constexpr (FUSED) {
-#pragma unroll
-              for (int r = 0; r < 4; ++r) v[r] += dpp_f32<0x128>(v[r]);
-            }
-            v *= f[q];
-            if (!FUSED || m < 8) {
-#pragma unroll
-              for (int r = 0; r < 4; ++r) so[wave][row + 16 * q][(4 * g + r) * TP + i % TP] = v[r];
-            }
-          }
-        }
+      for (int w = 0; w < kWaves; ++w) {
+        sum += so[w][r][q];
+        tot += sl[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - rb);
       }
-      __syncthreads();
-      for (int e = threadIdx.x; e < R * TP * 16; e += kThreads) {
-        const int r = e / (TP * 16), q = e % (TP * 16);
-        // place q: lane row q / TP, tile p TP + q % TP
-        const int qm = q / TP, i = p * TP + q % TP;
-        const int ch = D == 64 ? 8 * (qm >> 1) + (qm & 1) + 2 * i : qm * NT + i;
-        if (ch >= hd) continue;
-        float RM = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) RM = fmaxf(RM, sm[w][r]);
-        const float rb = RM == -INFINITY ? 0.f : RM;
-        float sum = 0.f, tot = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          sum += so[w][r][q];
-          tot += sl[w][r] * __builtin_amdgcn_exp2f(sm[w][r] - rb);
-        }
-        if (a.splits == 1) {
-          a.out[(int64_t)(s.first + r / a.group) * a.out_stride + (int64_t)(kvh * a.group + r % a.group) * hd + ch] =
-              tot == 0.f ? 0.f : sum / tot;
-        } else {
-          a.part[(slot0 + r) * hd + ch] = sum;
-          if (ch == 0) ml[2 * (slot0 + r)] = RM, ml[2 * (slot0 + r) + 1] = tot;
-        }
+      if (a.splits == 1) {
+        a.out[(int64_t)(s.first + r / a.group) * a.out_stride + (int64_t)(kvh * a.group + r % a.group) * hd + ch] =
+            tot == 0.f ? 0.f : sum / tot;
+      } else {
+        a.part[(slot0 + r) * hd + ch] = sum;
+        if (ch == 0) ml[2 * (slot0 + r)] = RM, ml[2 * (slot0 + r) + 1] = tot;
       }
     }
-    __syncthreads();  // before the next sequence writes sm, sl
   }
 }
 
@@ -650,7 +648,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
   // kv heads fastest: neighbours in the grid go to different XCDs, so each
   // XCD's L2 holds few heads. Later rows see more keys and start first.
   const int kvh = blockIdx.x % c.n_kv, rest = blockIdx.x / c.n_kv;
-  const int split = rest % a.splits, slot = rest / a.splits, slots = gridDim.x / (c.n_kv * a.splits);
+  const int split = rest % a.splits, slot = rest / a.splits;
   const int hd = c.hd, lg = c.page_log2, P = 1 << lg, row_b = hd / 2;
   const int scale_at = kv4_code_bytes(hd, lg), part_b = kv4_part_bytes(hd, lg);
   const int64_t head_at = kv4_part(c, kvh, 0);
@@ -676,303 +674,301 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attn_tile_kernel(At
   const int vwrite = C::KBYTES + vrow * C::VROW + 2 * sub_key + 16 * (kg & 1) + 8 * (kg >> 1);
   const int kread = m * C::KROW + 16 * h, vread = C::KBYTES + m * C::VROW + 16 * h;
 
-  for (int64_t place = slot; place < a.places; place += slots) {
-    int b, row0;
-    SeqRows s;
-    if (a.row_tiles > 0) {
-      b = (int)(place / a.row_tiles);
-      row0 = (a.row_tiles - 1 - (int)(place - (int64_t)b * a.row_tiles)) * kTileRows;
-      s = seq_rows(c, b);
+  const int64_t place = a.first + slot;
+  int b, row0;
+  SeqRows s;
+  if (a.row_tiles > 0) {
+    b = (int)(place / a.row_tiles);
+    row0 = (a.row_tiles - 1 - (int)(place - (int64_t)b * a.row_tiles)) * kTileRows;
+    s = seq_rows(c, b);
+  } else {
+    row0 = ragged_place(a, place, &b, &s);
+  }
+  const int n = s.n < a.max_q ? s.n : a.max_q;
+  const int R = n * a.group;
+  if (row0 < 0 || row0 >= R) return;
+  const int len = clamped_len(a, s.len), pos0 = len - s.n;
+  const int rlast = (row0 + kTileRows < R ? row0 + kTileRows : R) - 1;
+  const Seen first = seen_keys(a, pos0 + row0 / a.group, len), last = seen_keys(a, pos0 + rlast / a.group, len);
+  const int lo = first.lo & ~(KT - 1), hi = last.hi;
+  const int tiles = hi > first.lo ? (hi - lo + KT - 1) / KT : 0;
+  const int each = (int)((unsigned)tiles / (unsigned)a.splits), more = tiles - each * a.splits;
+  const int tile0 = split * each + (split < more ? split : more), tile1 = tile0 + each + (split < more ? 1 : 0);
+  const int32_t* table = c.table + (int64_t)b * c.table_stride;
+
+  const int row = row0 + wave * 32 + m;
+  const bool row_on = row < R;
+  const int tok = row_on ? row / a.group : 0;
+  const int head = kvh * a.group + (row_on ? row - tok * a.group : 0);
+  const Seen mine = seen_keys(a, pos0 + tok, len);
+  const bool wave_on = row0 + wave * 32 < R;  // else the wave only brings keys and values in
+
+  typename RowTile<D>::Codes raw_v[4];
+  uint32_t raw_k[KW], none = 0;
+  uint16_t raw_ks;
+  u32x2 raw_vs;
+  // The page of the wave's keys in the tile that is fetched next. It is the
+  // same in all lanes, but is kept in a vector register until then (the zero
+  // that the compiler cannot see through): a scalar one would be waited for
+  // where it is loaded, and with it all loads in flight.
+  int zero, id_v = 0;
+  __asm__("v_mov_b32 %0, 0" : "=v"(zero));
+  const auto find = [&](int tile) {
+    const int key = lo + tile * KT + sub_key;
+    id_v = table[((key < hi ? key : hi - 1) >> lg) + zero];
+  };
+  const auto fetch = [&](int tile) {
+    const int id = __builtin_amdgcn_readfirstlane(id_v);
+    const int slot0 = (lo + tile * KT + sub_key) & (P - 1);
+    const bool ok = id >= 0 && id < c.n_pages;  // else nothing is read, and the scores are NaN
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        c.pages + (int64_t)(ok ? id : 0) * c.page_bytes + head_at, 0, ok ? 2 * part_b : 0, kBufferFlags);
+    const int code_at = slot0 * row_b, scales = scale_at + 2 * slot0;
+    if constexpr (KW == 2) {
+      const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, koff, code_at, 0));
+      raw_k[0] = v.x, raw_k[1] = v.y;
     } else {
-      row0 = ragged_place(a, place, &b, &s);
-    }
-    const int n = s.n < a.max_q ? s.n : a.max_q;
-    const int R = n * a.group;
-    if (row0 < 0 || row0 >= R) continue;
-    const int len = clamped_len(a, s.len), pos0 = len - s.n;
-    const int rlast = (row0 + kTileRows < R ? row0 + kTileRows : R) - 1;
-    const Seen first = seen_keys(a, pos0 + row0 / a.group, len), last = seen_keys(a, pos0 + rlast / a.group, len);
-    const int lo = first.lo & ~(KT - 1), hi = last.hi;
-    const int tiles = hi > first.lo ? (hi - lo + KT - 1) / KT : 0;
-    const int each = (int)((unsigned)tiles / (unsigned)a.splits), more = tiles - each * a.splits;
-    const int tile0 = split * each + (split < more ? split : more), tile1 = tile0 + each + (split < more ? 1 : 0);
-    const int32_t* table = c.table + (int64_t)b * c.table_stride;
-
-    const int row = row0 + wave * 32 + m;
-    const bool row_on = row < R;
-    const int tok = row_on ? row / a.group : 0;
-    const int head = kvh * a.group + (row_on ? row - tok * a.group : 0);
-    const Seen mine = seen_keys(a, pos0 + tok, len);
-    const bool wave_on = row0 + wave * 32 < R;  // else the wave only brings keys and values in
-
-    typename RowTile<D>::Codes raw_v[4];
-    uint32_t raw_k[KW], none = 0;
-    uint16_t raw_ks;
-    u32x2 raw_vs;
-    // The page of the wave's keys in the tile that is fetched next. It is the
-    // same in all lanes, but is kept in a vector register until then (the zero
-    // that the compiler cannot see through): a scalar one would be waited for
-    // where it is loaded, and with it all loads in flight.
-    int zero, id_v = 0;
-    __asm__("v_mov_b32 %0, 0" : "=v"(zero));
-    const auto find = [&](int tile) {
-      const int key = lo + tile * KT + sub_key;
-      id_v = table[((key < hi ? key : hi - 1) >> lg) + zero];
-    };
-    const auto fetch = [&](int tile) {
-      const int id = __builtin_amdgcn_readfirstlane(id_v);
-      const int slot0 = (lo + tile * KT + sub_key) & (P - 1);
-      const bool ok = id >= 0 && id < c.n_pages;  // else nothing is read, and the scores are NaN
-      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          c.pages + (int64_t)(ok ? id : 0) * c.page_bytes + head_at, 0, ok ? 2 * part_b : 0, kBufferFlags);
-      const int code_at = slot0 * row_b, scales = scale_at + 2 * slot0;
-      if constexpr (KW == 2) {
-        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, koff, code_at, 0));
-        raw_k[0] = v.x, raw_k[1] = v.y;
-      } else {
-        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, koff, code_at, 0));
+      const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, koff, code_at, 0));
 #pragma unroll
-        for (int w = 0; w < 4; ++w) raw_k[w] = v[w];
-      }
-      raw_ks = __builtin_amdgcn_raw_buffer_load_b16(rs, ksoff, scales, 0);
-      none = ok ? 0u : 0x7E00u;
+      for (int w = 0; w < 4; ++w) raw_k[w] = v[w];
+    }
+    raw_ks = __builtin_amdgcn_raw_buffer_load_b16(rs, ksoff, scales, 0);
+    none = ok ? 0u : 0x7E00u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (D == 64)
+        raw_v[j] = __builtin_amdgcn_raw_buffer_load_b16(rs, voff, part_b + code_at + j * row_b, 0);
+      else
+        raw_v[j] = __builtin_amdgcn_raw_buffer_load_b32(rs, voff, part_b + code_at + j * row_b, 0);
+    }
+    raw_vs = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, vsoff, part_b + scales, 0));
+  };
+  const auto masked = [&](int tile) {
+    const int key0 = lo + tile * KT;
+    return key0 + KT > first.hi || key0 < last.lo;
+  };
+  const auto stage = [&](int tile) {
+    uint8_t* buf = lds[tile & 1];
+    if (masked(tile + 1) && tid == 0) bad[(tile + 1) % 3] = 0;
+    {
+      const h2 d = both(raw_ks | none), off = minus8(d);
+#pragma unroll
+      for (int w = 0; w < KW; ++w)
+        *reinterpret_cast<h8*>(buf + kwrite + 16 * w) = key_operand(raw_k[w], d, off);
+    }
+    if (masked(tile)) {
+      const int key0 = lo + tile * KT + sub_key + 4 * kg;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if constexpr (D == 64)
-          raw_v[j] = __builtin_amdgcn_raw_buffer_load_b16(rs, voff, part_b + code_at + j * row_b, 0);
-        else
-          raw_v[j] = __builtin_amdgcn_raw_buffer_load_b32(rs, voff, part_b + code_at + j * row_b, 0);
+        const uint32_t bits = (raw_vs[j >> 1] >> (16 * (j & 1))) & 0xFFFF;
+        const bool out = key0 + j >= hi, inf = (bits & 0x7C00) == 0x7C00;
+        if (inf && !out) atomicOr(&bad[tile % 3], 1ull << (sub_key + 4 * kg + j));
+        if (inf || out) raw_vs[j >> 1] &= j & 1 ? 0x0000FFFFu : 0xFFFF0000u;
       }
-      raw_vs = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, vsoff, part_b + scales, 0));
-    };
-    const auto masked = [&](int tile) {
-      const int key0 = lo + tile * KT;
-      return key0 + KT > first.hi || key0 < last.lo;
-    };
-    const auto stage = [&](int tile) {
-      uint8_t* buf = lds[tile & 1];
-      if (masked(tile + 1) && tid == 0) bad[(tile + 1) % 3] = 0;
-      {
-        const h2 d = both(raw_ks | none), off = minus8(d);
+    }
+    const h2 d0 = __builtin_bit_cast(h2, (uint32_t)raw_vs.x), d1 = __builtin_bit_cast(h2, (uint32_t)raw_vs.y);
+    const h2 off0 = minus8(d0), off1 = minus8(d1);
 #pragma unroll
-        for (int w = 0; w < KW; ++w)
-          *reinterpret_cast<h8*>(buf + kwrite + 16 * w) = key_operand(raw_k[w], d, off);
+    for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
+      const uint32_t sel = half ? 0x07030602u : 0x05010400u;
+      const uint32_t y0 = __builtin_amdgcn_perm(raw_v[1], raw_v[0], sel), y1 = __builtin_amdgcn_perm(raw_v[3], raw_v[2], sel);
+      const uint32_t lo0 = y0 & 0x0F0F0F0Fu, lo1 = y1 & 0x0F0F0F0Fu;
+      const uint32_t hi0 = (y0 >> 4) & 0x0F0F0F0Fu, hi1 = (y1 >> 4) & 0x0F0F0F0Fu;
+      const auto put = [&](int i, h2 u, h2 v) {  // channel 2 i + half of the dword (D = 64: 2 i + m16 & 1)
+        u32x2 x = {__builtin_bit_cast(uint32_t, u), __builtin_bit_cast(uint32_t, v)};
+        *reinterpret_cast<u32x2*>(buf + vwrite + (2 * i + half) * (D / 8) * C::VROW) = x;
+      };
+      put(0, two_values<0>(lo0, d0, off0), two_values<0>(lo1, d1, off1));
+      put(1, two_values<0>(hi0, d0, off0), two_values<0>(hi1, d1, off1));
+      put(2, two_values<1>(lo0, d0, off0), two_values<1>(lo1, d1, off1));
+      put(3, two_values<1>(hi0, d0, off0), two_values<1>(hi1, d1, off1));
+    }
+  };
+
+  if (tid < 3) bad[tid] = 0;
+  if (tile0 < tile1) {
+    find(tile0);
+    fetch(tile0);
+    find(tile0 + 1);
+  }
+
+  // the query operand, hi and lo parts
+  h8 qh[KS], ql[KS];
+  float down;
+  {
+    const float* qr = a.q + (int64_t)(s.first + tok) * a.q_stride + (int64_t)head * hd;
+    float big = 0.f;
+#pragma unroll
+    for (int w = 0; w < KS; ++w) {
+      const int c0 = 16 * w + 8 * h;
+      const bool in = row_on && c0 < hd;
+      const f32x4 u = load_f32x4(qr + (in ? c0 : 0)), v = load_f32x4(qr + (in ? c0 + 4 : 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) big = fmaxf(big, in ? fmaxf(__builtin_fabsf(u[i]), __builtin_fabsf(v[i])) : 0.f);
+    }
+    const RowScale rs = row_scale(fmaxf(big, __shfl_xor(big, 32)), a.scale);
+    down = rs.down;
+#pragma unroll
+    for (int w = 0; w < KS; ++w) {
+      const int c0 = 16 * w + 8 * h;
+      const bool in = row_on && c0 < hd;
+      const f32x4 u = load_f32x4(qr + (in ? c0 : 0)), v = load_f32x4(qr + (in ? c0 + 4 : 4));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e = slot_channel(j);
+        const float y = in ? (e < 4 ? u[e & 3] : v[e & 3]) * rs.up : 0.f;
+        qh[w][j] = (_Float16)y;
+        ql[w][j] = (_Float16)(y - (float)qh[w][j]);
       }
+    }
+  }
+
+  f32x16 o[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
+  float mx = -INFINITY, l = 0.f;
+
+  float minus1 = -1.f;  // kept from being folded, so that p - hi and its rounding are one v_fma_mix
+  __asm__("" : "+s"(minus1));
+  __syncthreads();  // bad is clear
+  if (tile0 < tile1) {
+    stage(tile0);
+    fetch(tile0 + 1);  // (past the last tile, its page again)
+    find(tile0 + 2);
+  }
+  __syncthreads();
+  for (int tile = tile0; tile < tile1; ++tile) {
+    const uint8_t* buf = lds[tile & 1];
+    const int key0 = lo + tile * KT;
+    // 32 keys at a time, which keeps the scores and weights in 32 registers.
+    // Operands are asked for in LDS two products ahead, the first ones of the
+    // values before the softmax (two prompts of about 4096 positions, 32
+    // heads: 440 us without, 420 with one ahead, 417 with two).
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      if (!wave_on) break;
+      f32x16 sc = {};
+      __builtin_amdgcn_sched_barrier(0);
+      const uint8_t* kb = buf + kread + 32 * k * C::KROW;
+      constexpr int AHEAD = 2;
+      h8 x[AHEAD + 1];
+#pragma unroll
+      for (int w = 0; w < AHEAD; ++w) x[w] = *reinterpret_cast<const h8*>(kb + 32 * w);
+#pragma unroll
+      for (int w = 0; w < KS; ++w) {
+        if (w + AHEAD < KS) x[(w + AHEAD) % (AHEAD + 1)] = *reinterpret_cast<const h8*>(kb + 32 * (w + AHEAD));
+        __builtin_amdgcn_sched_barrier(0);
+        sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[w % (AHEAD + 1)], qh[w], sc, 0, 0, 0);
+        sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[w % (AHEAD + 1)], ql[w], sc, 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      const auto v_at = [&](int u) {
+        return *reinterpret_cast<const h8*>(buf + vread + 32 * (u % NT) * C::VROW + 32 * (2 * k + u / NT));
+      };
+#pragma unroll
+      for (int u = 0; u < 2; ++u) x[u] = v_at(u);
+      __builtin_amdgcn_sched_barrier(0);
       if (masked(tile)) {
-        const int key0 = lo + tile * KT + sub_key + 4 * kg;
+        // (keys counted from the lane's first one, so that all that differs
+        // between its scores are constants)
+        const uint32_t bm = (uint32_t)(bad[tile % 3] >> (32 * k)) >> (4 * h);
+        const int from = mine.lo - (key0 + 32 * k + 4 * h), to = mine.hi - (key0 + 32 * k + 4 * h);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t bits = (raw_vs[j >> 1] >> (16 * (j & 1))) & 0xFFFF;
-          const bool out = key0 + j >= hi, inf = (bits & 0x7C00) == 0x7C00;
-          if (inf && !out) atomicOr(&bad[tile % 3], 1ull << (sub_key + 4 * kg + j));
-          if (inf || out) raw_vs[j >> 1] &= j & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+        for (int r = 0; r < 16; ++r) {
+          const int at = 8 * (r >> 2) + (r & 3);
+          if (bm >> at & 1) sc[r] = __builtin_nanf("");
+          if (at < from || at >= to) sc[r] = -INFINITY;
         }
       }
-      const h2 d0 = __builtin_bit_cast(h2, (uint32_t)raw_vs.x), d1 = __builtin_bit_cast(h2, (uint32_t)raw_vs.y);
-      const h2 off0 = minus8(d0), off1 = minus8(d1);
+      float top = sc[0];
 #pragma unroll
-      for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
-        const uint32_t sel = half ? 0x07030602u : 0x05010400u;
-        const uint32_t y0 = __builtin_amdgcn_perm(raw_v[1], raw_v[0], sel), y1 = __builtin_amdgcn_perm(raw_v[3], raw_v[2], sel);
-        const uint32_t lo0 = y0 & 0x0F0F0F0Fu, lo1 = y1 & 0x0F0F0F0Fu;
-        const uint32_t hi0 = (y0 >> 4) & 0x0F0F0F0Fu, hi1 = (y1 >> 4) & 0x0F0F0F0Fu;
-        const auto put = [&](int i, h2 u, h2 v) {  // channel 2 i + half of the dword (D = 64: 2 i + m16 & 1)
-          u32x2 x = {__builtin_bit_cast(uint32_t, u), __builtin_bit_cast(uint32_t, v)};
-          *reinterpret_cast<u32x2*>(buf + vwrite + (2 * i + half) * (D / 8) * C::VROW) = x;
-        };
-        put(0, two_values<0>(lo0, d0, off0), two_values<0>(lo1, d1, off1));
-        put(1, two_values<0>(hi0, d0, off0), two_values<0>(hi1, d1, off1));
-        put(2, two_values<1>(lo0, d0, off0), two_values<1>(lo1, d1, off1));
-        put(3, two_values<1>(hi0, d0, off0), two_values<1>(hi1, d1, off1));
+      for (int r = 1; r < 16; ++r) top = fmaxf(top, sc[r]);
+      {
+        const uint32_t u = __builtin_bit_cast(uint32_t, top);
+        const auto both_halves = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        top = fmaxf(__builtin_bit_cast(float, (uint32_t)both_halves[0]),
+                    __builtin_bit_cast(float, (uint32_t)both_halves[1])) * down;
       }
-    };
-
-    if (tid < 3) bad[tid] = 0;
-    if (tile0 < tile1) {
-      find(tile0);
-      fetch(tile0);
-      find(tile0 + 1);
-    }
-
-    // the query operand, hi and lo parts
-    h8 qh[KS], ql[KS];
-    float down;
-    {
-      const float* qr = a.q + (int64_t)(s.first + tok) * a.q_stride + (int64_t)head * hd;
-      float big = 0.f;
+      if (__any(top > mx + kSlack)) {
+        const float nm = fmaxf(mx, top);
+        const float f = __builtin_amdgcn_exp2f(mx - (nm == -INFINITY ? 0.f : nm));
+        mx = nm;
+        l *= f;
 #pragma unroll
-      for (int w = 0; w < KS; ++w) {
-        const int c0 = 16 * w + 8 * h;
-        const bool in = row_on && c0 < hd;
-        const f32x4 u = load_f32x4(qr + (in ? c0 : 0)), v = load_f32x4(qr + (in ? c0 + 4 : 4));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) big = fmaxf(big, in ? fmaxf(__builtin_fabsf(u[i]), __builtin_fabsf(v[i])) : 0.f);
+        for (int i = 0; i < NT; ++i) o[i] *= f;
       }
-      const RowScale rs = row_scale(fmaxf(big, __shfl_xor(big, 32)), a.scale);
-      down = rs.down;
+      const float base = mx == -INFINITY ? 0.f : mx;
+      h8 ph[2], pl[2];
 #pragma unroll
-      for (int w = 0; w < KS; ++w) {
-        const int c0 = 16 * w + 8 * h;
-        const bool in = row_on && c0 < hd;
-        const f32x4 u = load_f32x4(qr + (in ? c0 : 0)), v = load_f32x4(qr + (in ? c0 + 4 : 4));
+      for (int t = 0; t < 2; ++t) {
+        h2 hs[4], ls[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = slot_channel(j);
-          const float y = in ? (e < 4 ? u[e & 3] : v[e & 3]) * rs.up : 0.f;
-          qh[w][j] = (_Float16)y;
-          ql[w][j] = (_Float16)(y - (float)qh[w][j]);
+        for (int r = 0; r < 4; ++r) {
+          const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * t + 2 * r], down, -base));
+          const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * t + 2 * r + 1], down, -base));
+          l += p0 + p1;
+          hs[r] = hi_parts(p0, p1);
+          ls[r] = lo_parts(hs[r], p0, p1, minus1);
         }
-      }
-    }
-
-    f32x16 o[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
-    float mx = -INFINITY, l = 0.f;
-
-    float minus1 = -1.f;  // kept from being folded, so that p - hi and its rounding are one v_fma_mix
-    __asm__("" : "+s"(minus1));
-    __syncthreads();  // bad is clear
-    if (tile0 < tile1) {
-      stage(tile0);
-      fetch(tile0 + 1);  // (past the last tile, its page again)
-      find(tile0 + 2);
-    }
-    __syncthreads();
-    for (int tile = tile0; tile < tile1; ++tile) {
-      const uint8_t* buf = lds[tile & 1];
-      const int key0 = lo + tile * KT;
-      // 32 keys at a time, which keeps the scores and weights in 32 registers.
-      // Operands are asked for in LDS two products ahead, the first ones of the
-      // values before the softmax (two prompts of about 4096 positions, 32
-      // heads: 440 us without, 420 with one ahead, 417 with two).
-#pragma unroll
-      for (int k = 0; k < KB; ++k) {
-        if (!wave_on) break;
-        f32x16 sc = {};
-        __builtin_amdgcn_sched_barrier(0);
-        const uint8_t* kb = buf + kread + 32 * k * C::KROW;
-        constexpr int AHEAD = 2;
-        h8 x[AHEAD + 1];
-#pragma unroll
-        for (int w = 0; w < AHEAD; ++w) x[w] = *reinterpret_cast<const h8*>(kb + 32 * w);
-#pragma unroll
-        for (int w = 0; w < KS; ++w) {
-          if (w + AHEAD < KS) x[(w + AHEAD) % (AHEAD + 1)] = *reinterpret_cast<const h8*>(kb + 32 * (w + AHEAD));
-          __builtin_amdgcn_sched_barrier(0);
-          sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[w % (AHEAD + 1)], qh[w], sc, 0, 0, 0);
-          sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[w % (AHEAD + 1)], ql[w], sc, 0, 0, 0);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        const auto v_at = [&](int u) {
-          return *reinterpret_cast<const h8*>(buf + vread + 32 * (u % NT) * C::VROW + 32 * (2 * k + u / NT));
-        };
-#pragma unroll
-        for (int u = 0; u < 2; ++u) x[u] = v_at(u);
-        __builtin_amdgcn_sched_barrier(0);
-        if (masked(tile)) {
-          // (keys counted from the lane's first one, so that all that differs
-          // between its scores are constants)
-          const uint32_t bm = (uint32_t)(bad[tile % 3] >> (32 * k)) >> (4 * h);
-          const int from = mine.lo - (key0 + 32 * k + 4 * h), to = mine.hi - (key0 + 32 * k + 4 * h);
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int at = 8 * (r >> 2) + (r & 3);
-            if (bm >> at & 1) sc[r] = __builtin_nanf("");
-            if (at < from || at >= to) sc[r] = -INFINITY;
-          }
-        }
-        float top = sc[0];
-#pragma unroll
-        for (int r = 1; r < 16; ++r) top = fmaxf(top, sc[r]);
-        {
-          const uint32_t u = __builtin_bit_cast(uint32_t, top);
-          const auto both_halves = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-          top = fmaxf(__builtin_bit_cast(float, (uint32_t)both_halves[0]),
-                      __builtin_bit_cast(float, (uint32_t)both_halves[1])) * down;
-        }
-        if (__any(top > mx + kSlack)) {
-          const float nm = fmaxf(mx, top);
-          const float f = __builtin_amdgcn_exp2f(mx - (nm == -INFINITY ? 0.f : nm));
-          mx = nm;
-          l *= f;
-#pragma unroll
-          for (int i = 0; i < NT; ++i) o[i] *= f;
-        }
-        const float base = mx == -INFINITY ? 0.f : mx;
-        h8 ph[2], pl[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          h2 hs[4], ls[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * t + 2 * r], down, -base));
-            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[8 * t + 2 * r + 1], down, -base));
-            l += p0 + p1;
-            hs[r] = hi_parts(p0, p1);
-            ls[r] = lo_parts(hs[r], p0, p1, minus1);
-          }
-          ph[t] = as_h8(hs[0], hs[1], hs[2], hs[3]);
-          pl[t] = as_h8(ls[0], ls[1], ls[2], ls[3]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int u = 2; u < AHEAD; ++u) x[u] = v_at(u);
-#pragma unroll
-        for (int u = 0; u < 2 * NT; ++u) {
-          if (u + AHEAD < 2 * NT) x[(u + AHEAD) % (AHEAD + 1)] = v_at(u + AHEAD);
-          __builtin_amdgcn_sched_barrier(0);
-          o[u % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[u % (AHEAD + 1)], ph[u / NT], o[u % NT], 0, 0, 0);
-          o[u % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[u % (AHEAD + 1)], pl[u / NT], o[u % NT], 0, 0, 0);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+        ph[t] = as_h8(hs[0], hs[1], hs[2], hs[3]);
+        pl[t] = as_h8(ls[0], ls[1], ls[2], ls[3]);
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (tile + 1 < tile1) {
-        stage(tile + 1);
+#pragma unroll
+      for (int u = 2; u < AHEAD; ++u) x[u] = v_at(u);
+#pragma unroll
+      for (int u = 0; u < 2 * NT; ++u) {
+        if (u + AHEAD < 2 * NT) x[(u + AHEAD) % (AHEAD + 1)] = v_at(u + AHEAD);
         __builtin_amdgcn_sched_barrier(0);
-        fetch(tile + 2);
-        find(tile + 3);
+        o[u % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[u % (AHEAD + 1)], ph[u / NT], o[u % NT], 0, 0, 0);
+        o[u % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[u % (AHEAD + 1)], pl[u / NT], o[u % NT], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __syncthreads();
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (tile + 1 < tile1) {
+      stage(tile + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(tile + 2);
+      find(tile + 3);
+    }
+    __syncthreads();
+  }
 
-    l += __shfl_xor(l, 32);
-    if (row_on) {
-      const int64_t slot = ((((int64_t)b * c.n_kv + kvh) * a.splits + split) * a.max_q) * a.group + row;
-      float* out;
-      float f = 1.f;
-      if (a.splits == 1) {
-        out = a.out + (int64_t)(s.first + tok) * a.out_stride + (int64_t)head * hd;
-        f = l == 0.f ? 0.f : 1.f / l;
-      } else {
-        out = a.part + slot * hd;
-        float* ml = a.part + (int64_t)c.n_seq * c.n_kv * a.splits * a.max_q * a.group * hd + 2 * slot;
-        if (h == 0) ml[0] = mx, ml[1] = l;
+  l += __shfl_xor(l, 32);
+  if (row_on) {
+    const int64_t slot = ((((int64_t)b * c.n_kv + kvh) * a.splits + split) * a.max_q) * a.group + row;
+    float* out;
+    float f = 1.f;
+    if (a.splits == 1) {
+      out = a.out + (int64_t)(s.first + tok) * a.out_stride + (int64_t)head * hd;
+      f = l == 0.f ? 0.f : 1.f / l;
+    } else {
+      out = a.part + slot * hd;
+      float* ml = a.part + (int64_t)c.n_seq * c.n_kv * a.splits * a.max_q * a.group * hd + 2 * slot;
+      if (h == 0) ml[0] = mx, ml[1] = l;
+    }
+    // value row r of matrix tile i is channel (32 i + r) / (D / 8) of dword
+    // (32 i + r) % (D / 8): a lane holds all 8 channels of D / 16 dwords
+    constexpr int W = D / 8, RUNS = D / 16;
+#pragma unroll
+    for (int e = 0; e < RUNS; ++e) {
+      // rows with r & 3 = e & 3, and (r >> 2) = e >> 2 modulo W / 8
+      float x[8];
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch) {
+        const int r0 = ch * W + 8 * (e >> 2) + (e & 3);  // without 4 h
+        x[ch] = o[r0 / 32][4 * ((r0 % 32) / 8) + (e & 3)] * f;
       }
-      // value row r of matrix tile i is channel (32 i + r) / (D / 8) of dword
-      // (32 i + r) % (D / 8): a lane holds all 8 channels of D / 16 dwords
-      constexpr int W = D / 8, RUNS = D / 16;
-#pragma unroll
-      for (int e = 0; e < RUNS; ++e) {
-        // rows with r & 3 = e & 3, and (r >> 2) = e >> 2 modulo W / 8
-        float x[8];
-#pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {
-          const int r0 = ch * W + 8 * (e >> 2) + (e & 3);  // without 4 h
-          x[ch] = o[r0 / 32][4 * ((r0 % 32) / 8) + (e & 3)] * f;
-        }
-        const int w = 8 * (e >> 2) + 4 * h + (e & 3);
-        if (w * 8 < hd) {
-          const f32x4 u = {x[0], x[1], x[2], x[3]}, v = {x[4], x[5], x[6], x[7]};
-          __builtin_memcpy(__builtin_assume_aligned(out + w * 8, 4), &u, 16);
-          __builtin_memcpy(__builtin_assume_aligned(out + w * 8 + 4, 4), &v, 16);
-        }
+      const int w = 8 * (e >> 2) + 4 * h + (e & 3);
+      if (w * 8 < hd) {
+        const f32x4 u = {x[0], x[1], x[2], x[3]}, v = {x[4], x[5], x[6], x[7]};
+        __builtin_memcpy(__builtin_assume_aligned(out + w * 8, 4), &u, 16);
+        __builtin_memcpy(__builtin_assume_aligned(out + w * 8 + 4, 4), &v, 16);
       }
     }
-    __syncthreads();  // before the next sequence clears bad
   }
 }
 
@@ -1073,23 +1069,25 @@ void launch_join(const AttnArgs& a, int64_t rows, hipStream_t s) {
                        dim3(kThreads), 0, s, a);
 }
 
-// The grid's second extent: the sequences, up to 2^22 workgroups in all and
-// the extent that HIP allows on every device; a workgroup goes on to the next ones.
-unsigned sequences_at_once(const AttnArgs& a, int64_t gx) {
-  return (unsigned)std::max<int64_t>(1, std::min<int64_t>({a.c.n_seq, (1 << 22) / gx, 65535}));
-}
-
 // Rows of a sequence and kv head up to which the row kernel is taken.
 constexpr int kRowKernelRows = 32;
 
+// One launch takes up to kMaxGrid workgroups, and kMaxSequences sequences in the
+// grid's second extent; more take several (a workgroup that loops over
+// sequences instead costs 20 registers and 2%).
+constexpr int64_t kMaxGrid = 1 << 22, kMaxSequences = 65535;
+
 template <int D>
-void launch_rows(const AttnArgs& a, hipStream_t s) {
+void launch_rows(AttnArgs a, hipStream_t s) {
   const int64_t rows = (int64_t)a.max_q * a.group;
   const int64_t gx = (int64_t)a.c.n_kv * a.splits;
-  const dim3 grid((unsigned)gx, sequences_at_once(a, gx));
-  if (rows <= 8) hipLaunchKernelGGL((attn_rows_kernel<D, 8>), grid, dim3(kThreads), 0, s, a);
-  else if (rows <= 16) hipLaunchKernelGGL((attn_rows_kernel<D, 16>), grid, dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((attn_rows_kernel<D, 32>), grid, dim3(kThreads), 0, s, a);
+  const int64_t most = std::max<int64_t>(1, std::min(kMaxGrid / gx, kMaxSequences));
+  for (a.first = 0; a.first < a.c.n_seq; a.first += most) {
+    const dim3 grid((unsigned)gx, (unsigned)std::min<int64_t>(most, a.c.n_seq - a.first));
+    if (rows <= 8) hipLaunchKernelGGL((attn_rows_kernel<D, 8>), grid, dim3(kThreads), 0, s, a);
+    else if (rows <= 16) hipLaunchKernelGGL((attn_rows_kernel<D, 16>), grid, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((attn_rows_kernel<D, 32>), grid, dim3(kThreads), 0, s, a);
+  }
 }
 
 // The grid counts places for row tiles. Where sequences have about the same
@@ -1109,8 +1107,9 @@ void launch_tiles(AttnArgs a, hipStream_t s) {
   a.row_tiles = !a.c.q_start || a.c.n_seq * tiles <= ragged ? (int)tiles : 0;
   a.places = a.row_tiles ? a.c.n_seq * tiles : ragged;
   const int64_t heads = (int64_t)a.c.n_kv * a.splits;
-  const int64_t slots = std::max<int64_t>(1, std::min(a.places, (1 << 22) / heads));
-  hipLaunchKernelGGL((attn_tile_kernel<D>), dim3((unsigned)(heads * slots)), dim3(kThreads), 0, s, a);
+  const int64_t most = std::max<int64_t>(1, kMaxGrid / heads);
+  for (a.first = 0; a.first < a.places; a.first += most)
+    hipLaunchKernelGGL((attn_tile_kernel<D>), dim3((unsigned)(heads * std::min(most, a.places - a.first))), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace
