@@ -154,9 +154,9 @@ __device__ __forceinline__ RowScale row_scale(float largest, float scale) {
 // Bound: HBM, nearly. 32 sequences of 8k to 16k keys, 8 kv heads of 128 and 4
 // query heads each (452 MB): 92 us, 4.9 TB/s; its loads alone take 84 us (with
 // cached or nontemporal loads alike), its arithmetic alone 70 (about 1500
-// cycles of issue per 32 keys and SIMD). Three waves a SIMD (128 channels) hide
-// one under the other; four, with fewer registers, took 107 us, a second tile
-// of registers in flight spilled (209). One sequence of 8192 keys: 8.7 us.
+// cycles of issue per 32 keys and SIMD). Four waves a SIMD (128 channels) hide
+// one under the other as well as three do, and a second tile of registers in
+// flight gives nothing. One sequence of 8192 keys: 8.2 us.
 template <int D>
 struct RowTile {
   static constexpr int KW = D / 32;             // dwords of a key per lane
@@ -579,7 +579,7 @@ __global__ __launch_bounds__(kThreads, row_kernel_waves(D, ROWS)) void attn_rows
 //   whose keys are ordered as the scores lie: chunk 2 t + h of a value row
 //   holds keys 16 t + 4 h + 0 .. 3 and 16 t + 8 + 4 h + 0 .. 3.
 // Bound: the matrix cores, and what of the vector work is not under them. Two
-// prompts of 4096 and 2895 positions, 32 / 8 heads of 128: 390 us, 526 TFLOP/s
+// prompts of 4096 and 2895 positions, 32 / 8 heads of 128: 384 us, 537 TFLOP/s
 // of the formula's operations and twice that with the lo parts. Without softmax
 // and staging the same kernel took 352 us, the rate of a large library product
 // (1170 TFLOP/s; the clock falls to 1.9 GHz under it); the vector work alone
