@@ -1,0 +1,145 @@
+"""Randomized sweep of the rotary positions, the 4-bit cache and its attention
+on the GPU, for a time budget: every case draws a ragged batch (1..40
+sequences, rows from none to 400, lengths from none to 6000), a page size, head
+counts, a head size, a rotation, masks and bounds from a seeded generator;
+appends the rows and compares every byte of the pool with the 64-bit oracle,
+reads them back, attends over the cache and checks a sample of rows within
+their bounds and that rows of no sequence are left as they were. Prints each
+case before running it and exits 1 on any failure. Not collected by pytest;
+run it on a machine with a GPU:
+
+    python tests/fuzz_kv4.py [--seconds 120] [--seed 5]
+"""
+import argparse
+import os
+import sys
+import time
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+sys.path.insert(0, os.path.dirname(HERE))
+sys.path.insert(0, HERE)
+
+import numpy as np  # noqa: E402
+
+
+def main() -> int:
+    ap = argparse.ArgumentParser()
+    ap.add_argument("--seconds", type=float, default=120.0)
+    ap.add_argument("--seed", type=int, default=5)
+    args = ap.parse_args()
+
+    import torch
+
+    import gguf_block_quant_gq_amd as gq
+    import oracle.kv4 as o
+    from kv4_helpers import HALF, Batch, check_attention, to_dev, to_host
+
+    torch.cuda.set_device(0)
+    failures, case, worst = 0, 0, 0.0
+    t_end = time.time() + args.seconds
+    while time.time() < t_end:
+        case += 1
+        rng = np.random.default_rng([args.seed, case])
+        pick = lambda *x: x[int(rng.integers(len(x)))]  # noqa: E731
+        log = lambda lo, hi: int(np.exp(rng.uniform(np.log(lo), np.log(hi + 1))))  # noqa: E731
+        hd = 32 * int(rng.integers(1, 9))
+        n_kv, group = pick(1, 1, 2, 3, 4), pick(1, 2, 3, 4, 5, 7, 8, 16, 33)
+        H, P = n_kv * group, 16 << int(rng.integers(7))
+        n_seq = log(1, 40)
+        uniform = rng.random() < 0.3
+        longest = 1 if uniform else log(1, max(1, 400 // n_seq))
+        n = [1] * n_seq if uniform else [int(rng.integers(0, longest + 1)) for _ in range(n_seq)]
+        if not sum(n):
+            n[0] = 1
+        deep = log(1, max(2, 6000 // n_seq))
+        lens = [m + int(rng.integers(0, deep)) for m in n]
+        rot = 2 * int(rng.integers(0, hd // 2 + 1)) if rng.random() < 0.5 else hd
+        inter, normed = rng.random() < 0.5, rng.random() < 0.5
+        causal, window = rng.random() < 0.8, pick(0, 0, 0, log(1, 4000))
+        front, back = int(rng.integers(0, 4)) * (not uniform), int(rng.integers(0, 4)) * (not uniform)
+        b = Batch(1000 + case, n, lens, P, n_kv, hd, uniform=uniform)
+        extra = int(rng.integers(0, 40))
+        b.table = np.concatenate((b.table, np.full((n_seq, extra), 1 << 29, np.int32)), 1)
+        max_len = pick(max(lens), b.table.shape[1] * P)
+        max_q = pick(None, max(n), max(n) + 5)
+        print(f"[{case}] n={n} lens={lens} P={P} H={H}/{n_kv} hd={hd} rot={rot} inter={inter} norm={normed} causal={causal} "
+              f"window={window} max_len={max_len} max_q={max_q} rows {front}+{b.n_tok}+{back}", flush=True)
+
+        # append, all bytes; queries; read back
+        total = front + b.n_tok + back
+        x = rng.standard_normal((total, H + 2 * n_kv, hd)).astype(np.float32)
+        w = [(1 + 0.1 * rng.standard_normal(hd)).astype(np.float32) if normed else None for _ in range(2)]
+        freqs = (10000.0 ** (-np.arange(0, rot, 2) / max(rot, 1))).astype(np.float32)
+        rope = gq.Rope(to_dev(freqs), interleaved=inter, mscale=1.125) if rot else None
+        lens_d, q_start = b.dev()
+        if q_start is not None:
+            q_start = q_start + front
+        cache, dev = b.cache(gq), to_dev(x)
+        q = gq.gq_kv4_append(cache, dev[:, H:H + n_kv], dev[:, H + n_kv:], lens_d, q_start, rope=rope,
+                             k_norm=None if w[1] is None else to_dev(w[1]), q=dev[:, :H],
+                             q_norm=None if w[0] is None else to_dev(w[0]), q_out=dev[:, :H])
+        where = [None] * front + o.rows(b.q_start, b.lens, b.n_tok) + [None] * back
+        pos = [0 if p is None else p[1] for p in where]
+        turned = o.rope(x[:, H:H + n_kv], pos, freqs, inter, 1.125, w[1])
+        want = b.pages.copy()
+        for t, p in enumerate(where):
+            if p is not None:
+                for h in range(n_kv):
+                    page = int(b.table[p[0], p[1] // P])
+                    o.store(want, page, p[1] % P, P, hd, h, 0, turned[t, h])
+                    o.store(want, page, p[1] % P, P, hd, h, 1, x[t, H + n_kv + h])
+        got = to_host(cache.pages).reshape(want.shape)
+        if not np.array_equal(got, want):
+            failures += 1
+            print(f"  FAIL append: {int((got != want).sum())} bytes differ", flush=True)
+        gq_ = to_host(q)
+        qr = o.rope(x[:, :H], pos, freqs, inter, 1.125, w[0])
+        for t, p in enumerate(where):
+            if p is None:
+                bad = not np.array_equal(gq_[t], x[t, :H])
+            else:
+                tol = HALF * np.abs(qr[t]) + 2.0 ** -44 * 2.5 * np.abs(qr).max() + 2.0 ** -149
+                bad = (np.abs(gq_[t].astype(np.float64) - qr[t]) > tol).any()
+            if bad:
+                failures += 1
+                print(f"  FAIL queries of row {t}", flush=True)
+                break
+        b.pages = want
+        K = torch.full((total, n_kv, hd), 9.0, device="cuda")
+        V = K.clone()
+        gq.gq_kv4_read(cache, lens_d, total, q_start, K=K, V=V)
+        K, V = to_host(K), to_host(V)
+        seqs = {}
+        for t, p in enumerate(where):
+            if p is None:
+                bad = not ((K[t] == 9.0).all() and (V[t] == 9.0).all())
+            else:
+                if p[0] not in seqs:
+                    seqs[p[0]] = b.sequence(p[0])
+                bad = not (np.array_equal(K[t], seqs[p[0]][0][p[1]]) and np.array_equal(V[t], seqs[p[0]][1][p[1]]))
+            if bad:
+                failures += 1
+                print(f"  FAIL read of row {t}", flush=True)
+                break
+
+        # attention, a sample of rows
+        out = torch.full((total, H, hd), 7.0, device="cuda")
+        scale = float(pick(hd ** -0.5, 1.0, 0.02))
+        gq.gq_kv4_attn(cache, q, lens_d, q_start, max_q=max_q, max_len=max_len, scale=scale, causal=causal, window=window, out=out)
+        got = to_host(out)
+        if not (got[:front] == 7.0).all() or not (got[total - back:] == 7.0).all():
+            failures += 1
+            print("  FAIL attention wrote rows of no sequence", flush=True)
+        mine = gq_[front:total - back] if not uniform else gq_
+        rows = sorted({0, b.n_tok - 1} | {int(r) for r in rng.integers(0, b.n_tok, 6)})
+        try:
+            worst = max(worst, check_attention(b, got[front:total - back], mine, scale, causal, window, rows=rows))
+        except AssertionError as e:
+            failures += 1
+            print(f"  FAIL attention: {e}", flush=True)
+    print(f"{case} cases, {failures} failures, attention at most {worst:.3f} of its bound (seed {args.seed})", flush=True)
+    return 1 if failures else 0
+
+
+if __name__ == "__main__":
+    sys.exit(main())
