@@ -1145,8 +1145,9 @@ void launch_tiles(AttnArgs a, hipStream_t s) {
 //     512, 8 kv heads: 28.5 us whole, 31.7 in two);
 //   - two for a few more workgroups than that and 2048 keys or more (a prompt of
 //     3000 tokens, 16 heads: 108 us against 130; 2048 tokens, 4 kv heads of 256:
-//     133 against 158; 1500 tokens 89 against 119; but 512 workgroups of 128
-//     channels: 106 against 90).
+//     133 against 158; 1500 tokens 89 against 119; 4096 tokens, 2 kv heads of 64,
+//     448 workgroups: 88 against 107; but 512 workgroups of 128 channels over
+//     2048 keys: 106 against 90).
 int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len, int hd) {
   if (n_seq <= 0 || rows <= 0) return 1;
   if (rows <= kRowKernelRows) {
@@ -1162,6 +1163,7 @@ int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len, 
   else if (n_seq > 1) fill = std::max(fill, std::min(max_len / 1000, 512 / base));
   if (max_len - max_len / fill <= 256) fill = 1;
   if (fill == 1 && max_len >= 2048 && base <= (hd <= 128 ? 384 : 256)) fill = 2;
+  if (fill == 1 && max_len >= 3300 && base <= (hd <= 64 ? 512 : hd <= 128 ? 448 : 256)) fill = 2;
   if (fill == 1 && max_len >= 1024 && hd > 128 && base <= 192) fill = 2;
   return (int)fill;
 }
