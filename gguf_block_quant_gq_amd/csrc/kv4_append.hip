@@ -185,7 +185,7 @@ __global__ __launch_bounds__(kThreads) void qk_rope_kernel(QkArgs a) {
   __shared__ uint8_t* pages[TOK];
   __shared__ int where[TOK];           // positions; -1: the row belongs to none
   constexpr int kHeads = kThreads / GL;  // heads per pass
-  static_assert(TOK <= kThreads / 64, "a wave looks up each token");
+  static_assert(TOK <= 2 && TOK <= kThreads / 64, "a wave looks up each token");
   const int tid = threadIdx.x, sub = tid % GL, slot = tid / GL;
   const int hd = a.hd, c0 = sub * 8, half = a.r.half;
   const bool lane_on = c0 < hd;
@@ -238,6 +238,11 @@ __global__ __launch_bounds__(kThreads) void qk_rope_kernel(QkArgs a) {
       }
       if (first) {  // the angles, with the loads above in flight
         first = false;
+        // this thread's pair, whose frequency arrives under the look-up
+        static_assert(TOK * kMaxPairs <= kThreads, "a thread per token and pair");
+        const int pk = TOK == 1 || tid < half ? 0 : 1, pp = tid - pk * half;
+        const bool turns = tid < toks * half;
+        const float freq = turns ? a.r.freqs[pp] : 0.f;
         __syncthreads();  // the tokens before have been turned
         uint8_t* page = nullptr;
         const int mine = tid >> 6;  // the token that this wave looks up (TOK is at most the waves)
@@ -250,12 +255,9 @@ __global__ __launch_bounds__(kThreads) void qk_rope_kernel(QkArgs a) {
           }
           __syncthreads();
         }
-        for (int i = tid; i < TOK * half; i += kThreads) {
-          const int k = TOK == 1 ? 0 : i / half, p = i - k * half;
-          if (k < toks) {
-            const int pos = APPEND ? where[k] : a.pos[t0 + k];
-            turn[k][p] = sin_cos((double)pos * (double)a.r.freqs[p]) * (double)a.r.mscale;
-          }
+        if (turns) {
+          const int pos = APPEND ? where[pk] : a.pos[t0 + pk];
+          turn[pk][pp] = sin_cos((double)pos * (double)freq) * (double)a.r.mscale;
         }
         if (APPEND && mine < toks && (tid & 63) == 0) pages[mine] = page;
         __syncthreads();
