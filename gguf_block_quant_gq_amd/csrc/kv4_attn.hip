@@ -1129,8 +1129,10 @@ void launch_tiles(AttnArgs a, hipStream_t s) {
 //   - for two workgroups a CU, if all have 360 keys or more (4 such sequences
 //     of 8192 keys: 16.8 us in 16 parts, 17.6 in 8, 19.4 in 32; 8 of 2500:
 //     13.9 us in 4, 15.1 in 7);
-//   - none where they would not save a wave 448 keys / 4 (16 sequences of 700
-//     keys: 11.5 us whole, 12.7 in two; one of 333 keys: 8.1, 9.6 in four);
+//   - none where they would not save a workgroup 448 keys (16 sequences of 700
+//     keys: 11.5 us whole, 12.7 in two; one of 333 keys: 8.1, 9.6 in four), or
+//     300 or 200 where a step takes longer (32 rows, one sequence of 500 keys,
+//     heads of 128: 16.7 us whole, 13.8 in four; 8 heads of 256: 13.7, 12.5);
 //   - of 1024 keys or more up to 2048 workgroups, to even out sequences of
 //     different lengths (32 sequences of 8k to 16k keys: 99.7 us, 105 with
 //     1024 workgroups, 117 with 512).
@@ -1157,7 +1159,9 @@ int kv4_attn_splits(int64_t n_seq, int64_t n_kv, int64_t rows, int64_t max_len, 
     const int64_t base = n_seq * n_kv;
     int64_t fill = std::max<int64_t>(1, std::min((max_len + 127) / 128, 256 / base));
     if (max_len >= 360 * (512 / base)) fill = std::max(fill, 512 / base);
-    if (max_len - max_len / fill < 448) fill = 1;
+    const int slow = (rows > 8) + (rows > 16) + (hd > 128) - (hd <= 64);
+    const int64_t worth = slow <= 0 ? 448 : slow == 1 ? 300 : 200;
+    if (max_len - max_len / fill < worth) fill = 1;
     return (int)std::max(fill, std::min((max_len + 512) / 1024, 2048 / base));
   }
   const int64_t base = n_seq * n_kv * ((rows + kTileRows - 1) / kTileRows);
