@@ -583,7 +583,7 @@ __global__ __launch_bounds__(kThreads, row_kernel_waves(D, ROWS)) void attn_rows
 // of the formula's operations and twice that with the lo parts. Without softmax
 // and staging the same kernel took 352 us, the rate of a large library product
 // (1170 TFLOP/s; the clock falls to 1.9 GHz under it); the vector work alone
-// takes 275, of which about 40 us stay exposed. The matrix cores and the vector
+// takes 275, of which about 30 us stay exposed. The matrix cores and the vector
 // unit work at once only for different waves of a SIMD, hence two workgroups a
 // CU; 256 rows and 8 waves to a workgroup (one barrier for both waves of a
 // SIMD) took 553 us against 464, wave priorities made no difference.
